@@ -203,6 +203,62 @@ MOE_API moe_status_t moe_forward(moe_dims_t d, const uint16_t* x, const uint16_t
                          moe_weight_t W1, const uint16_t* b1, moe_weight_t W2, const uint16_t* b2,
                          uint16_t* y, void* ws, size_t ws_bytes, void* stream);
 
+/* The whole layer for a few tokens (a decode step) in one launch: the same
+ * definition and arguments as moe_forward, for T <= moe_few_max_tokens(d).
+ * Defined by: as moe_forward.
+ * One cooperative kernel streams the weights of the experts the tokens route
+ * to once, as stored (bf16, or MXFP4 codes and scales: data and scales are
+ * required, a prepared form is not read). Logits and expert outputs are fp32,
+ * h is rounded to bf16; MXFP4 codes are multiplied exactly with activations
+ * that keep bf16's precision, so the output is that of the dequantised
+ * weights. Equal logits go to the lower expert index, a NaN logit below every
+ * number; an infinity or NaN in a token's row reaches only that token's
+ * output. Deterministic for given sizes; its sums are ordered differently from
+ * moe_forward's. The kernel needs every SM of the device at once: it starts
+ * when the kernels before it on the device have left enough room (another
+ * stream's long kernel delays it). Returns MOE_ERR_UNSUPPORTED for more
+ * tokens. */
+MOE_API moe_status_t moe_forward_few(moe_dims_t d, const uint16_t* x, const uint16_t* Wr, const uint16_t* br,
+                             moe_weight_t W1, const uint16_t* b1, moe_weight_t W2, const uint16_t* b2,
+                             uint16_t* y, void* ws, size_t ws_bytes, void* stream);
+
+/* The most tokens moe_forward_few takes for d's layer (d.T is not read):
+ * min(16, 65536 / max(D, I)), 0 if d is invalid. */
+MOE_API int32_t moe_few_max_tokens(moe_dims_t d);
+
+/* Element type of a tensor that may be held in either. */
+typedef enum { MOE_T_BF16 = 0, MOE_T_F32 = 1 } moe_type_t;
+
+/* T rows of D elements, consecutive rows of x ldx elements apart, the norm's
+ * eps, and the type of the residual stream (moe_type_t). */
+typedef struct {
+  int32_t T, D;
+  int64_t ldx;
+  float eps;
+  int32_t res_type;
+} moe_norm_t;
+
+/* RMSNorm with the residual's addition, as it stands in front of the layer.
+ * Defined by: from-scratch GPT-OSS write-up, "model flow" (residual addition
+ * and RMSNorm between attention and expert routing).
+ *   s = x + residual, rounded to the residual stream's type (s = x without one)
+ *   y = s * (mean(s^2) + eps)^-1/2 * gamma, computed in fp32
+ *   x (T,D) bf16 with rows ldx apart; residual (T,D) bf16 or fp32, or NULL;
+ *   gamma (D) bf16
+ *   -> res_out (T,D) in the residual's type = s (may be NULL, may be the
+ *      residual's own buffer; NULL without a residual);
+ *      y (T,D) bf16 (may be NULL);
+ *      q (T,D) E4M3 and q_scale (T, ceil(D/128)) fp32 (may both be NULL): per
+ *      row and 128 columns c = max(max|y|, 2^-100) / 448, q = e4m3(y / c),
+ *      rounded to nearest even from the fp32 y -- the left operand of
+ *      moe_fp8_matmul. A NaN in a row makes that row NaN.
+ * At least one of y and q is given. No buffer but residual / res_out may
+ * overlap another. T >= 0 (T = 0: nothing is enqueued), D a multiple of 16 up
+ * to 16384, ldx >= D a multiple of 16, eps >= 0 and finite. Needs no
+ * workspace; deterministic. */
+MOE_API moe_status_t moe_rmsnorm(moe_norm_t n, const uint16_t* x, const void* residual, const uint16_t* gamma,
+                         void* res_out, uint16_t* y, uint8_t* q, float* q_scale, void* stream);
+
 /* The MXFP4 expert weights are multiplied as stored (E2M1 codes with E8M0
  * block scales, GPT-OSS in Transformers blog, MXFP4 paragraph) on block-scaled
  * tensor-core MMAs, which read the scales in their own layout: each MXFP4 GEMM

@@ -16,9 +16,10 @@ from ._binding import (  # noqa: F401
     alloc_workspace, check_dims,
     moe_route, moe_permute, moe_gather, moe_mlp1, moe_mlp2, moe_ffn_grouped, moe_combine, moe_forward,
     moe_read_device_status, status_str, moe_permute_noalloc, moe_selftest_wait_timeout, mxfp4_prepared_bytes,
-    moe_mxfp4_prepare, mxfp4_prepare,
+    moe_mxfp4_prepare, mxfp4_prepare, MOE_T_BF16, MOE_T_F32, NormDims, moe_forward_few, few_max_tokens, moe_rmsnorm,
 )
 from .ep import CudaLocalOps, ExpertParallelMoE, ep_forward  # noqa: F401,E402
+from .block import MoEBlock, rmsnorm, rmsnorm_fp8  # noqa: F401,E402
 
 
 class MoELayer:
@@ -67,6 +68,21 @@ class MoELayer:
         return y
 
     __call__ = forward
+
+    @property
+    def few_max_tokens(self) -> int:
+        """The most tokens forward_few takes."""
+        return few_max_tokens(self.dims(1))
+
+    def forward_few(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """forward for at most few_max_tokens tokens in one launch
+        (moe_forward_few): the latency path of a decode step. MXFP4 weights
+        are read as stored, so the layer keeps their codes and scales."""
+        T = x.shape[0]
+        y = out if out is not None else torch.empty((T, self.D), dtype=torch.bfloat16, device=x.device)
+        moe_forward_few(self.dims(T), x, self.Wr, self.br, self.W1, self.b1, self.W2, self.b2, y, self.workspace(T),
+                        W1_scales=self.W1_scales, W2_scales=self.W2_scales, stream=stream)
+        return y
 
     def device_status(self) -> int:
         return 0 if self._ws is None else moe_read_device_status(self._ws)

@@ -16,6 +16,7 @@ LIB_PATH = os.path.join(HERE, "libmoe.so")
 
 MOE_W_BF16, MOE_W_MXFP4 = 0, 1
 MOE_ACT_SWIGLU, MOE_ACT_GPTOSS = 0, 1
+MOE_T_BF16, MOE_T_F32 = 0, 1
 STATUS = {
     0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_WORKSPACE", 4: "MOE_ERR_CUDA",
     5: "MOE_ERR_TIMEOUT", 6: "MOE_ERR_DEVICE_BOUNDS",
@@ -24,7 +25,8 @@ STATUS = {
 # Every symbol include/moe.h declares.
 EXPORTS = ("moe_workspace_bytes", "moe_check_dims", "moe_route", "moe_permute", "moe_gather", "moe_mlp1", "moe_mlp2",
            "moe_ffn_grouped", "moe_combine", "moe_forward", "moe_read_device_status", "moe_status_str",
-           "moe_permute_noalloc", "moe_selftest_wait_timeout", "moe_mxfp4_prepared_bytes", "moe_mxfp4_prepare")
+           "moe_permute_noalloc", "moe_selftest_wait_timeout", "moe_mxfp4_prepared_bytes", "moe_mxfp4_prepare",
+           "moe_forward_few", "moe_few_max_tokens", "moe_rmsnorm")
 
 
 class MoeError(RuntimeError):
@@ -41,6 +43,11 @@ class Dims(ctypes.Structure):
 
 class Weight(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("prepared", ctypes.c_void_p)]
+
+
+class NormDims(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("D", ctypes.c_int32), ("ldx", ctypes.c_int64), ("eps", ctypes.c_float),
+                ("res_type", ctypes.c_int32)]
 
 
 _lib = None
@@ -75,6 +82,9 @@ def load(path: str = LIB_PATH):
         "moe_selftest_wait_timeout": (ctypes.c_int, [VP, ctypes.c_uint64, VP]),
         "moe_status_str": (ctypes.c_char_p, [ctypes.c_int]),
         "moe_mxfp4_prepared_bytes": (ctypes.c_size_t, [Dims, ctypes.c_int32]),
+        "moe_forward_few": (ctypes.c_int, [Dims, VP, VP, VP, Weight, VP, Weight, VP, VP, VP, ctypes.c_size_t, VP]),
+        "moe_few_max_tokens": (ctypes.c_int32, [Dims]),
+        "moe_rmsnorm": (ctypes.c_int, [NormDims, VP, VP, VP, VP, VP, VP, VP, VP]),
         "moe_mxfp4_prepare": (ctypes.c_int, [Dims, ctypes.c_int32, Weight, VP, ctypes.c_size_t, VP]),
     }
     for name, (res, args) in sig.items():
@@ -165,6 +175,21 @@ def moe_forward(d, x, Wr, br, W1, b1, W2, b2, y, ws, W1_scales=None, W2_scales=N
                 W2_prepared=None):
     _check(load().moe_forward(d, _p(x), _p(Wr), _p(br), _w(W1, W1_scales, W1_prepared), _p(b1), _w(W2, W2_scales, W2_prepared), _p(b2), _p(y),
                               _p(ws), ws.numel(), _stream(stream)), "moe_forward")
+
+
+def moe_forward_few(d, x, Wr, br, W1, b1, W2, b2, y, ws, W1_scales=None, W2_scales=None, stream=None):
+    """moe_forward for at most few_max_tokens(d) tokens, in one launch."""
+    _check(load().moe_forward_few(d, _p(x), _p(Wr), _p(br), _w(W1, W1_scales), _p(b1), _w(W2, W2_scales), _p(b2), _p(y),
+                                  _p(ws), ws.numel(), _stream(stream)), "moe_forward_few")
+
+
+def few_max_tokens(d: Dims) -> int:
+    return load().moe_few_max_tokens(d)
+
+
+def moe_rmsnorm(n: NormDims, x, residual, gamma, res_out, y, q, q_scale, stream=None):
+    _check(load().moe_rmsnorm(n, _p(x), _p(residual), _p(gamma), _p(res_out), _p(y), _p(q), _p(q_scale),
+                              _stream(stream)), "moe_rmsnorm")
 
 
 def moe_permute_noalloc(d, topk_idx, counts, offsets, perm, inv, stream=None):

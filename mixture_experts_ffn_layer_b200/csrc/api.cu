@@ -1,6 +1,7 @@
 // The C ABI of include/moe.h: argument validation, workspace layout, and the
 // enqueueing of the kernels of route.cu, permute.cu, grouped_gemm.cu,
-// grouped_gemm_pair.cu and mx_gemm.cu on the caller's stream.
+// grouped_gemm_pair.cu, mx_gemm.cu, norm.cu, few.cu and fp8_gemm.cu on the
+// caller's stream.
 // No host synchronisation except in moe_read_device_status.
 #include <cmath>
 
@@ -13,7 +14,7 @@ namespace {
 
 struct WsLayout {
   size_t block_counts, topk_idx, topk_w, counts, offsets, perm, inv, x_perm, h, o_perm, xq, x_sf, hq, h_sf,
-      mx_prep, route_partial, total;
+      mx_prep, route_partial, few_logits, few_done, total;
 };
 
 WsLayout ws_layout(const moe_dims_t& d) {
@@ -45,6 +46,10 @@ WsLayout ws_layout(const moe_dims_t& d) {
     L.hq = take(static_cast<size_t>(R) * d.I * 2);
     L.h_sf = take(mx_sf_bytes(d, d.I));
     L.mx_prep = take(mx_prep_bytes(d));
+  }
+  if (d.T <= few_max_tokens(d)) {  // the one-launch layer: its logits and completion counters
+    L.few_logits = take(static_cast<size_t>(d.T) * d.E * 4);
+    L.few_done = take(static_cast<size_t>(d.D) / 16 * 4);
   }
   L.total = off;
   return L;
@@ -256,6 +261,41 @@ moe_status_t moe_forward(moe_dims_t d, const uint16_t* x, const uint16_t* Wr, co
   MOE_TRY(moe_permute(d, topk_idx, counts, offsets, perm, inv, ws, ws_bytes, stream));
   MOE_TRY(moe_ffn_grouped(d, x, perm, offsets, topk_w, W1, b1, W2, b2, o_perm, ws, ws_bytes, stream));
   return moe_combine(d, o_perm, inv, y, ws, ws_bytes, stream);
+}
+
+int32_t moe_few_max_tokens(moe_dims_t d) {
+  d.T = 1;
+  if (moe_check_dims(d) != MOE_OK) return 0;
+  return few_max_tokens(d);
+}
+
+moe_status_t moe_forward_few(moe_dims_t d, const uint16_t* x, const uint16_t* Wr, const uint16_t* br, moe_weight_t W1,
+                             const uint16_t* b1, moe_weight_t W2, const uint16_t* b2, uint16_t* y, void* ws,
+                             size_t ws_bytes, void* stream) {
+  MOE_TRY(moe_check_dims(d));
+  if (d.T > few_max_tokens(d)) return MOE_ERR_UNSUPPORTED;
+  MOE_REQUIRE(x && Wr && br && b1 && b2 && y && W1.data && W2.data);
+  MOE_REQUIRE(aligned32(x) && aligned32(Wr) && aligned32(br) && aligned32(b1) && aligned32(b2) && aligned32(y));
+  MOE_TRY(check_weight(d, W1));
+  MOE_TRY(check_weight(d, W2));
+  MOE_REQUIRE(d.wfmt == MOE_W_BF16 || (W1.scales && W2.scales));  // the weights are read as stored
+  MOE_TRY(check_ws(d, ws, ws_bytes));
+  const WsLayout L = ws_layout(d);
+  return launch_few(d, x, Wr, br, W1, b1, W2, b2, y, at<float>(ws, L.few_logits), at<uint16_t>(ws, L.h),
+                    at<float>(ws, L.o_perm), at<unsigned>(ws, L.few_done), ws, static_cast<cudaStream_t>(stream));
+}
+
+moe_status_t moe_rmsnorm(moe_norm_t n, const uint16_t* x, const void* residual, const uint16_t* gamma, void* res_out,
+                         uint16_t* y, uint8_t* q, float* q_scale, void* stream) {
+  MOE_REQUIRE(n.T >= 0 && n.D > 0 && n.ldx >= n.D && std::isfinite(n.eps) && n.eps >= 0.0f);
+  MOE_REQUIRE(n.res_type == MOE_T_BF16 || n.res_type == MOE_T_F32);
+  if (n.D % 16 || n.ldx % 16 || n.D > 16384) return MOE_ERR_UNSUPPORTED;
+  if (n.T == 0) return MOE_OK;
+  MOE_REQUIRE(x && gamma && (y || q) && !q == !q_scale && (residual || !res_out));
+  MOE_REQUIRE(aligned32(x) && aligned32(residual) && aligned32(gamma) && aligned32(res_out) && aligned32(y) &&
+              aligned32(q) && aligned32(q_scale));
+  return cuda_status(
+      launch_rmsnorm(n, x, residual, gamma, res_out, y, q, q_scale, static_cast<cudaStream_t>(stream)));
 }
 
 size_t moe_mxfp4_prepared_bytes(moe_dims_t d, int32_t which) {

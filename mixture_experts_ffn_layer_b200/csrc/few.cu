@@ -1,0 +1,712 @@
+// The whole MoE layer for a few tokens (T <= 16) in one launch.
+//
+// A decode step reads the weights of the experts it routes to and little
+// else, so the layer is a stream of weights with a few rows of activations:
+// memory bound, and with eight launches between which nothing streams, latency
+// bound too. Here one cooperative kernel, one block per SM, does all of it:
+//
+//   1. router: one warp per (token, expert) logit, fp32 dot product;
+//      grid barrier; every block takes the top-k of all tokens itself (the
+//      same arithmetic everywhere) and lists the experts with rows.
+//   2. mlp1: the active experts' hidden units, 8 at a time (a granule: 8 gate
+//      rows and the 8 up rows of W1), are split evenly over the blocks; h
+//      (bf16, by assignment) goes to the workspace; grid barrier.
+//   3. mlp2: granules of 16 rows of W2, split the same way; the fp32 expert
+//      outputs go to the workspace, and the block that finishes the last
+//      expert of 16 output columns sums their k terms per token in slot order.
+//
+// A granule is 16 weight rows by the whole reduction. The block's 16 warps
+// split the reduction, so that every SM has work for as little as one token
+// and each warp meets the same slice of the activations in every granule.
+// Each warp streams its slices through its own cp.async ring (no block-wide
+// synchronisation to load; the ring keeps running across granules, experts
+// and from mlp1 into mlp2, whose first weights arrive while the grid barrier
+// is waited for) and multiplies them with mma.sync m16n8k16: the 16 weight
+// rows are M, up to 8 tokens are N (two N halves for more than 8). That is
+// the shape this work has -- a 128-row tensor tile would leave the SMs unevenly
+// loaded -- and the tensor rate is far from being a limit. The k index of an
+// MMA is permuted (lane q of a row's four holds 8 consecutive elements of a
+// 32-element unit), the same for weights and activations, so both are read
+// with wide shared-memory loads.
+//
+// MXFP4: a unit of 32 codes is one scale block. The codes become f16 (exact),
+// the activations f16 with one power of two per row such that the largest
+// magnitude is in [2^8, 2^9) (exact down to 2^-25 of it, absolute error below
+// 2^-33 of it), and each unit's fp32 sum is added with its weight scale.
+//
+// All sums are fp32. The order is fixed by the sizes, so results are bitwise
+// reproducible.
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "sm100.cuh"
+#include "tma_host.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kWarps = 16;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxT = 16;
+constexpr int kMaxK = 8;
+constexpr int kMaxActive = kMaxT * kMaxK;
+constexpr int kMaxSmem = 232448;      // 227 KB per block
+constexpr int kMaxStages = 8;
+constexpr int64_t kMaxRowBytes = 65536 * 2;  // T * max(D, I) bf16 of resident activations
+constexpr uint64_t kBarrierNs = 1000000000ull;
+
+// Grid-barrier state in the workspace header (the status word is at byte 0).
+constexpr int kBarCount = 16, kBarGen = 17;  // as 32-bit words
+
+template <int kFmt>
+struct Fmt;
+template <>
+struct Fmt<MOE_W_BF16> {
+  static constexpr int kUnitBytes = 64;           // 32 bf16
+  static constexpr int kUnits = 2;                // units per warp and stage: 128 bytes of a row
+  static constexpr int kPitch = 128;              // 16-byte chunks swizzled by row parity
+  static constexpr int kScalePitch = 0;
+};
+template <>
+struct Fmt<MOE_W_MXFP4> {
+  static constexpr int kUnitBytes = 16;           // 32 codes
+  static constexpr int kUnits = 6;
+  static constexpr int kPitch = 112;              // odd multiple of 16: 8 rows on distinct banks
+  static constexpr int kScalePitch = 12;          // aligned words covering kUnits scale bytes
+};
+template <int kFmt>
+constexpr int slot_bytes() {
+  return 16 * (Fmt<kFmt>::kPitch + Fmt<kFmt>::kScalePitch);
+}
+
+struct FewParams {
+  int T, D, E, k, I;
+  const uint16_t *x, *Wr, *br, *b1, *b2;
+  const uint8_t *w1, *w2, *s1, *s2;
+  float* logits;     // (T, E)
+  uint16_t* h;       // (T*k, I) bf16, by assignment
+  float* o;          // (T*k, D) fp32, by assignment, gate weight applied
+  unsigned* done;    // (D/16) expert granules finished
+  uint16_t* y;
+  unsigned* header;  // workspace header
+  int stages;
+  int row_pitch;     // bytes between resident activation rows
+  Act act;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// All but the newest n groups have landed.
+__device__ __forceinline__ void cp_wait_upto(int n) {
+  switch (n) {
+    case 1: cp_wait<1>(); break;
+    case 2: cp_wait<2>(); break;
+    case 3: cp_wait<3>(); break;
+    case 4: cp_wait<4>(); break;
+    case 5: cp_wait<5>(); break;
+    case 6: cp_wait<6>(); break;
+    case 7: cp_wait<7>(); break;
+    default: cp_wait<0>(); break;
+  }
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+
+__device__ __forceinline__ void mma_bf16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 8 E2M1 codes (low nibble first) -> 4 pairs of f16.
+__device__ __forceinline__ void e2m1_to_f16(uint32_t codes, uint32_t (&p)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(p[0]), "=r"(p[1]), "=r"(p[2]), "=r"(p[3])
+      : "r"(codes));
+}
+
+// E8M0: 2^(s - 127), the smallest a subnormal.
+__device__ __forceinline__ float e8m0(uint32_t s) { return __uint_as_float(s ? s << 23 : 0x00400000u); }
+
+// All blocks of the grid meet (the launch is cooperative, so all are
+// resident). The last to arrive resets the count, so the state is the same
+// after every barrier. Waits at most kBarrierNs, then records the timeout and
+// goes on: every index computed later is in range whatever the data hold.
+__device__ __forceinline__ void grid_barrier(unsigned* header) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    volatile unsigned* gen = header + kBarGen;
+    const unsigned g = *gen;
+    __threadfence();
+    if (atomicAdd(header + kBarCount, 1u) == gridDim.x - 1) {
+      atomicExch(header + kBarCount, 0u);
+      __threadfence();
+      atomicAdd(header + kBarGen, 1u);
+    } else {
+      const uint64_t t0 = sm100::globaltimer_ns();
+      for (uint32_t i = 1; *gen == g; ++i) {
+        if ((i & 255u) == 0 && sm100::globaltimer_ns() - t0 > kBarrierNs) {
+          record_status(reinterpret_cast<int*>(header), MOE_ERR_TIMEOUT);
+          break;
+        }
+      }
+    }
+    __threadfence();
+  }
+  __syncthreads();
+}
+
+// Order-preserving integer of a logit; NaN sorts below every number, -0 as +0.
+__device__ __forceinline__ uint32_t sort_key(float v) {
+  if (!(v == v)) return 0u;
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t key) {
+  if (key == 0u) return __uint_as_float(0x7fffffffu);
+  return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
+}
+
+struct FewShared {
+  int n_active;
+  uint16_t expert[kMaxActive];   // active experts, ascending
+  uint16_t tokens[kMaxActive];   // their tokens, a bit each
+  int16_t top[kMaxT][kMaxK];     // expert of each assignment
+  float gate[kMaxT][kMaxK];
+  int row[kMaxT];                // current expert: assignment of each resident row
+  uint32_t row_max[kMaxT];       // |largest| of each resident row (bf16 bits)
+  float row_scale[kMaxT];        // what a row's sums are multiplied with
+  int last[kMaxActive];
+};
+
+// One weight's granules as this block and warp see them.
+struct Stream {
+  const uint8_t *w, *s;
+  int64_t row_bytes;     // of the weight
+  int srow_bytes;        // of its scales
+  int rows;              // weight rows per expert
+  int up;                // row of the 9th weight row relative to the 1st (I: the up half; 8)
+  int step;              // weight rows a granule advances by (8 or 16)
+  int per_expert;        // granules per expert
+  int u0, u1;            // this warp's units of 32 of the reduction
+  int chunk;             // units per stage
+  int nchunks;           // stages per granule
+  int64_t g0, g1;        // this block's granules, over the active experts
+};
+
+template <int kFmt>
+__device__ __forceinline__ Stream make_stream(const FewParams& p, int which, int n_active, int warp) {
+  Stream s;
+  const int K = which == 1 ? p.D : p.I;
+  s.w = which == 1 ? p.w1 : p.w2;
+  s.s = which == 1 ? p.s1 : p.s2;
+  s.row_bytes = static_cast<int64_t>(K / 32) * Fmt<kFmt>::kUnitBytes;
+  s.srow_bytes = K / 32;
+  s.rows = which == 1 ? 2 * p.I : p.D;
+  s.up = which == 1 ? p.I : 8;
+  s.step = which == 1 ? 8 : 16;
+  s.per_expert = which == 1 ? p.I / 8 : p.D / 16;
+  const int units = K / 32, per = (units + kWarps - 1) / kWarps;
+  s.nchunks = (per + Fmt<kFmt>::kUnits - 1) / Fmt<kFmt>::kUnits;
+  s.chunk = (per + s.nchunks - 1) / s.nchunks;
+  s.u0 = min(units, warp * per);
+  s.u1 = min(units, s.u0 + per);
+  const int64_t n = static_cast<int64_t>(n_active) * s.per_expert;
+  s.g0 = n * blockIdx.x / gridDim.x;
+  s.g1 = n * (blockIdx.x + 1) / gridDim.x;
+  return s;
+}
+
+// Copy this warp's part of one stage (granule, chunk) into its ring slot.
+template <int kFmt>
+__device__ __forceinline__ void load_stage(const Stream& st, int expert, int local, int chunk, uint32_t slot,
+                                           int lane) {
+  constexpr int kU = Fmt<kFmt>::kUnits;
+  constexpr int kRowChunks = kU * Fmt<kFmt>::kUnitBytes / 16;  // 16-byte chunks of a row
+  const int u = st.u0 + chunk * st.chunk;
+  const int n = min(st.chunk, st.u1 - u);
+  if (n <= 0) return;
+  const int64_t row0 = static_cast<int64_t>(expert) * st.rows + static_cast<int64_t>(local) * st.step;
+  const uint8_t* base = st.w + row0 * st.row_bytes + static_cast<int64_t>(u) * Fmt<kFmt>::kUnitBytes;
+  const int valid = n * Fmt<kFmt>::kUnitBytes / 16;
+#pragma unroll
+  for (int i = 0; i < 16 * kRowChunks / 32; ++i) {
+    const int idx = lane + 32 * i;
+    const int r = idx / kRowChunks, c = idx % kRowChunks;
+    if (c < valid) {
+      const int wr = r < 8 ? r : st.up + r - 8;
+      const int cc = kFmt == MOE_W_BF16 ? c ^ ((r & 1) << 2) : c;
+      cp_async16(slot + r * Fmt<kFmt>::kPitch + cc * 16, base + wr * st.row_bytes + c * 16);
+    }
+  }
+  if (kFmt == MOE_W_MXFP4) {
+    // the aligned 4-byte words that hold each row's scale bytes [u, u + n)
+    // (the tensor's size is a multiple of 4, so they lie inside it)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int idx = lane + 32 * i;
+      const int r = idx / 3, c = idx % 3;
+      if (r < 16) {
+        const int wr = r < 8 ? r : st.up + r - 8;
+        const int64_t at = (row0 + wr) * st.srow_bytes + u;
+        const int64_t first = at & ~int64_t(3);
+        if (first + 4 * c < at + n)
+          cp_async4(slot + 16 * Fmt<kFmt>::kPitch + r * Fmt<kFmt>::kScalePitch + 4 * c, st.s + first + 4 * c);
+      }
+    }
+  }
+}
+
+// Multiply one landed stage: acc (kN groups of 8 tokens) += 16 weight rows x
+// the stage's units.
+template <int kFmt, int kN>
+__device__ __forceinline__ void mul_stage(const Stream& st, int expert, int local, int chunk, uint32_t slot,
+                                          uint32_t act, const uint32_t (&brow)[kN], int lane, float (&acc)[kN][4]) {
+  const int r = lane / 4, q = lane % 4;
+  const int u = st.u0 + chunk * st.chunk;
+  const int n = min(st.chunk, st.u1 - u);
+  if (n <= 0) return;
+  if (kFmt == MOE_W_BF16) {
+    // two units of a row are 8 chunks of 16 bytes: chunk 4*j + q, the halves
+    // exchanged in odd rows (conflict-free)
+#pragma unroll
+    for (int j = 0; j < Fmt<kFmt>::kUnits; ++j) {
+      if (j < n) {
+        const uint32_t off = static_cast<uint32_t>(((4 * j + q) ^ ((r & 1) << 2)) * 16);
+        const uint4 a = lds128(slot + r * Fmt<kFmt>::kPitch + off);
+        const uint4 a8 = lds128(slot + (r + 8) * Fmt<kFmt>::kPitch + off);
+#pragma unroll
+        for (int g = 0; g < kN; ++g) {
+          const uint4 b = lds128(act + brow[g] + (u + j) * 64 + q * 16);
+          mma_bf16_16816(acc[g], a.x, a8.x, a.y, a8.y, b.x, b.y);
+          mma_bf16_16816(acc[g], a.z, a8.z, a.w, a8.w, b.z, b.w);
+        }
+      }
+    }
+  } else {
+    const int64_t row0 = static_cast<int64_t>(expert) * st.rows + static_cast<int64_t>(local) * st.step;
+    const uint32_t sl = slot + 16 * Fmt<kFmt>::kPitch;
+    const uint32_t s_lo = sl + r * Fmt<kFmt>::kScalePitch +
+                          static_cast<uint32_t>(((row0 + r) * st.srow_bytes + u) & 3);
+    const uint32_t s_hi = sl + (r + 8) * Fmt<kFmt>::kScalePitch +
+                          static_cast<uint32_t>(((row0 + st.up + r) * st.srow_bytes + u) & 3);
+#pragma unroll
+    for (int j = 0; j < Fmt<kFmt>::kUnits; ++j) {
+      if (j < n) {
+        uint32_t a[4], a8[4];
+        e2m1_to_f16(lds32(slot + r * Fmt<kFmt>::kPitch + j * 16 + q * 4), a);
+        e2m1_to_f16(lds32(slot + (r + 8) * Fmt<kFmt>::kPitch + j * 16 + q * 4), a8);
+        const float w_lo = e8m0(lds8(s_lo + j)), w_hi = e8m0(lds8(s_hi + j));
+#pragma unroll
+        for (int g = 0; g < kN; ++g) {
+          const uint4 b = lds128(act + brow[g] + (u + j) * 64 + q * 16);
+          float c[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_f16_16816(c, a[0], a8[0], a[1], a8[1], b.x, b.y);
+          mma_f16_16816(c, a[2], a8[2], a[3], a8[3], b.z, b.w);
+          acc[g][0] = fmaf(w_lo, c[0], acc[g][0]);
+          acc[g][1] = fmaf(w_lo, c[1], acc[g][1]);
+          acc[g][2] = fmaf(w_hi, c[2], acc[g][2]);
+          acc[g][3] = fmaf(w_hi, c[3], acc[g][3]);
+        }
+      }
+    }
+  }
+}
+
+// Bring the rows of active expert `ai` into shared memory: x[t] (mlp1) or
+// h[a] (mlp2). MXFP4 rows become f16 scaled by a power of two.
+template <int kFmt>
+__device__ __forceinline__ void load_rows(const FewParams& p, FewShared& sh, int which, int ai, uint8_t* act) {
+  const int K = which == 1 ? p.D : p.I;
+  const int e = sh.expert[ai];
+  const uint32_t tokens = sh.tokens[ai];
+  const int rows = __popc(tokens);
+  if (threadIdx.x < rows) {
+    const int t = __fns(tokens, 0, threadIdx.x + 1);
+    int j = 0;
+    while (j < p.k - 1 && sh.top[t][j] != e) ++j;
+    sh.row[threadIdx.x] = t * p.k + j;
+    sh.row_max[threadIdx.x] = 0;
+  }
+  __syncthreads();
+  const int per = K / 8;  // 16-byte chunks per row
+  const int total = rows * per;
+  for (int base = threadIdx.x & ~31; base < total; base += kThreads) {  // (uniform in a warp)
+    const int i = base + (threadIdx.x & 31);
+    const bool on = i < total;
+    const int n = min(i, total - 1) / per, c = i - n * per;
+    uint32_t m = 0;
+    if (on) {
+      const int a = sh.row[n];
+      const uint4* src = reinterpret_cast<const uint4*>(which == 1 ? p.x + static_cast<int64_t>(a / p.k) * K
+                                                                   : p.h + static_cast<int64_t>(a) * K) + c;
+      const uint4 v = __ldcg(src);
+      *reinterpret_cast<uint4*>(act + n * p.row_pitch + c * 16) = v;
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int z = 0; z < 4; ++z) m = max(m, max(w[z] & 0x7fffu, (w[z] >> 16) & 0x7fffu));
+    }
+    if (kFmt == MOE_W_MXFP4) {
+      // a warp's chunks are consecutive: mostly of one row, then one atomic
+      if (__shfl_sync(0xffffffffu, n, 0) == __shfl_sync(0xffffffffu, n, 31)) {
+        m = __reduce_max_sync(0xffffffffu, m);
+        if ((threadIdx.x & 31) == 0) atomicMax(&sh.row_max[n], m);
+      } else if (on) {
+        atomicMax(&sh.row_max[n], m);
+      }
+    }
+  }
+  __syncthreads();
+  if (kFmt == MOE_W_MXFP4) {
+    for (int i = threadIdx.x; i < total; i += kThreads) {
+      const int n = i / per, c = i - n * per;
+      // 2^shift brings the row's largest magnitude into [2^8, 2^9); a row of
+      // zeros, or with an infinity or NaN, stays as it is
+      const int ex = static_cast<int>(sh.row_max[n] >> 7);  // biased exponent
+      const int shift = sh.row_max[n] == 0 || ex == 255 ? 0 : min(127, 8 + 127 - max(ex, 1));
+      const float mul = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
+      if (c == 0) sh.row_scale[n] = __uint_as_float(shift == 127 ? 0x00400000u : static_cast<uint32_t>(127 - shift) << 23);
+      uint4* at = reinterpret_cast<uint4*>(act + n * p.row_pitch + c * 16);
+      const uint4 v = *at;
+      uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        const __half2 h2 = __floats2half2_rn(__uint_as_float(w[z] << 16) * mul,
+                                             __uint_as_float(w[z] & 0xffff0000u) * mul);
+        w[z] = *reinterpret_cast<const uint32_t*>(&h2);
+      }
+      *at = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __syncthreads();
+  }
+}
+
+template <int kFmt, int kN>
+__global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  // resident rows | partial sums | rings
+  uint8_t* act = smem;
+  constexpr int kRedBufs = kN == 1 ? 2 : 1;
+  float* red = reinterpret_cast<float*>(smem + p.T * p.row_pitch);
+  constexpr int kRedFloats = kWarps * 128 * kN;
+  uint8_t* ring = reinterpret_cast<uint8_t*>(red + kRedBufs * kRedFloats);
+  __shared__ FewShared sh;
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  // ---- router logits, one warp each; the completion counters start at zero
+  for (int i = blockIdx.x * kThreads + threadIdx.x; i < p.D / 16; i += gridDim.x * kThreads) p.done[i] = 0;
+  for (int item = blockIdx.x * kWarps + warp; item < p.T * p.E; item += gridDim.x * kWarps) {
+    const int t = item / p.E, e = item - t * p.E;
+    const uint4* xr = reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(t) * p.D);
+    const uint4* wr = reinterpret_cast<const uint4*>(p.Wr + static_cast<int64_t>(e) * p.D);
+    float sum = 0.0f;
+#pragma unroll 6
+    for (int c = lane; c < p.D / 8; c += 32) {
+      const uint4 a = __ldg(xr + c), b = __ldg(wr + c);
+      const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        sum = fmaf(__uint_as_float(aw[z] << 16), __uint_as_float(bw[z] << 16), sum);
+        sum = fmaf(__uint_as_float(aw[z] & 0xffff0000u), __uint_as_float(bw[z] & 0xffff0000u), sum);
+      }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (lane == 0) p.logits[item] = sum + bf16_bits_to_float(p.br[e]);
+  }
+  grid_barrier(p.header);
+
+  // ---- top-k of every token (warp t), then the active experts
+  if (warp < p.T) {
+    uint32_t key[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = lane + 32 * i;
+      key[i] = e < p.E ? sort_key(__ldcg(p.logits + warp * p.E + e)) : 0u;
+    }
+    float first = 0.0f, total = 0.0f, mine = 0.0f;
+    uint32_t taken = 0;  // bit i: this lane's expert lane + 32 i is chosen already
+    for (int j = 0; j < p.k; ++j) {
+      uint32_t best = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (!((taken >> i) & 1u)) best = max(best, key[i]);
+      best = __reduce_max_sync(0xffffffffu, best);
+      uint32_t at = 0xffffffffu;  // lowest expert that holds it and is not taken
+#pragma unroll
+      for (int i = 7; i >= 0; --i)
+        if (!((taken >> i) & 1u) && key[i] == best && lane + 32 * i < p.E) at = lane + 32 * i;
+      at = __reduce_min_sync(0xffffffffu, at);
+      if (static_cast<int>(at & 31u) == lane) taken |= 1u << (at >> 5);
+      const float v = key_value(best);
+      if (j == 0) first = v;
+      const float ex = __expf(v - first);
+      total += ex;
+      if (lane == j) {
+        mine = ex;
+        sh.top[warp][j] = static_cast<int16_t>(at);
+      }
+    }
+    if (lane < p.k) sh.gate[warp][lane] = __fdividef(mine, total);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    // experts 32 i + lane: their tokens, and their place among the active ones
+    int n = 0;
+    for (int base = 0; base < p.E; base += 32) {
+      const int e = base + lane;
+      uint32_t tokens = 0;
+      for (int t = 0; t < p.T; ++t)
+        for (int j = 0; j < p.k; ++j)
+          if (sh.top[t][j] == e) tokens |= 1u << t;
+      const uint32_t has = __ballot_sync(0xffffffffu, tokens != 0);
+      if (tokens) {
+        const int at = n + __popc(has & ((1u << lane) - 1u));
+        sh.expert[at] = static_cast<uint16_t>(e);
+        sh.tokens[at] = static_cast<uint16_t>(tokens);
+      }
+      n += __popc(has);
+    }
+    if (lane == 0) sh.n_active = n;
+  }
+  __syncthreads();
+  const int n_active = sh.n_active;
+
+  // ---- the weight stream: mlp1's stages, then mlp2's, through this warp's ring
+  const Stream st1 = make_stream<kFmt>(p, 1, n_active, warp);
+  const Stream st2 = make_stream<kFmt>(p, 2, n_active, warp);
+  const uint32_t ring_at = sm100::smem_u32(ring) + warp * p.stages * slot_bytes<kFmt>();
+  // where the loads stand
+  int ld_phase = 1;
+  int64_t ld_g = st1.g0;
+  int ld_ai = static_cast<int>(ld_g / st1.per_expert), ld_local = static_cast<int>(ld_g % st1.per_expert), ld_chunk = 0;
+  int ld_slot = 0;
+  auto issue = [&]() {
+    if (ld_phase == 1 && ld_g >= st1.g1) {
+      ld_phase = 2;
+      ld_g = st2.g0;
+      ld_ai = static_cast<int>(ld_g / st2.per_expert);
+      ld_local = static_cast<int>(ld_g % st2.per_expert);
+      ld_chunk = 0;
+    }
+    const Stream& s = ld_phase == 1 ? st1 : st2;
+    if (ld_g < s.g1) {
+      load_stage<kFmt>(s, sh.expert[ld_ai], ld_local, ld_chunk, ring_at + ld_slot * slot_bytes<kFmt>(), lane);
+      if (++ld_chunk == s.nchunks) {
+        ld_chunk = 0;
+        ++ld_g;
+        if (++ld_local == s.per_expert) {
+          ld_local = 0;
+          ++ld_ai;
+        }
+      }
+    }
+    cp_commit();
+    if (++ld_slot == p.stages) ld_slot = 0;
+  };
+  for (int i = 0; i < p.stages; ++i) issue();
+
+  int slot = 0, buf = 0;
+  const uint32_t act_at = sm100::smem_u32(act);
+#pragma unroll 1
+  for (int which = 1; which <= 2; ++which) {
+    const Stream& s = which == 1 ? st1 : st2;
+    if (which == 2) grid_barrier(p.header);  // h is complete
+    int ai = static_cast<int>(s.g0 / s.per_expert), local = static_cast<int>(s.g0 % s.per_expert);
+    bool fresh = true;
+    for (int64_t g = s.g0; g < s.g1; ++g) {
+      if (fresh) {
+        __syncthreads();  // the previous expert's rows are read no more
+        load_rows<kFmt>(p, sh, which, ai, act);
+        fresh = false;
+      }
+      const int rows = __popc(static_cast<uint32_t>(sh.tokens[ai]));
+      const int e = sh.expert[ai];
+      uint32_t brow[kN];
+#pragma unroll
+      for (int i = 0; i < kN; ++i)  // a column without a token repeats the last row; its sums are not used
+        brow[i] = static_cast<uint32_t>(min(8 * i + lane / 4, rows - 1)) * p.row_pitch;
+      float acc[kN][4];
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[i][c] = 0.0f;
+      for (int chunk = 0; chunk < s.nchunks; ++chunk) {
+        cp_wait_upto(p.stages - 1);
+        __syncwarp();
+        mul_stage<kFmt, kN>(s, e, local, chunk, ring_at + slot * slot_bytes<kFmt>(), act_at, brow, lane, acc);
+        __syncwarp();
+        issue();
+        if (++slot == p.stages) slot = 0;
+      }
+      // sum the 16 warps' parts in warp order
+      float* part = red + buf * kRedFloats;
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        *reinterpret_cast<float4*>(part + (warp * kN + i) * 128 + lane * 4) =
+            make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      __syncthreads();
+      if (warp < 4 * kN) {
+        const int grp = warp / 4, at = threadIdx.x & 127;
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) v += part[(w * kN + grp) * 128 + at];
+        // fragment element -> weight row and token
+        const int src = at / 4, c = at % 4;
+        const int r = src / 4 + (c >= 2 ? 8 : 0), n = 8 * grp + (src % 4) * 2 + (c & 1);
+        const bool on = n < rows;
+        if (kFmt == MOE_W_MXFP4 && on) v *= sh.row_scale[n];
+        const int a = on ? sh.row[n] : 0;
+        if (which == 1) {
+          const float upv = __shfl_xor_sync(0xffffffffu, v, 2);
+          if (on && c < 2) {
+            const int i0 = local * 8 + r;
+            const uint16_t* bias = p.b1 + static_cast<int64_t>(e) * 2 * p.I;
+            const float gate = v + bf16_bits_to_float(bias[i0]), up = upv + bf16_bits_to_float(bias[p.I + i0]);
+            p.h[static_cast<int64_t>(a) * p.I + i0] = float_to_bf16_bits(glu_act(gate, up, p.act));
+          }
+        } else if (on) {
+          const int d0 = local * 16 + r;
+          const float wgt = sh.gate[a / p.k][a % p.k];
+          p.o[static_cast<int64_t>(a) * p.D + d0] =
+              wgt * (v + bf16_bits_to_float(p.b2[static_cast<int64_t>(e) * p.D + d0]));
+        }
+      }
+      if (kRedBufs == 1)
+        __syncthreads();  // one buffer: its readers are done before the next granule writes it
+      else
+        buf ^= 1;         // two: the next granule's barrier orders them
+      if (++local == s.per_expert) {
+        local = 0;
+        ++ai;
+        fresh = true;
+      }
+    }
+  }
+  cp_wait<0>();
+
+  // ---- combine: the block whose granule is the last of its 16 columns
+  __syncthreads();
+  const int n2 = static_cast<int>(st2.g1 - st2.g0);
+  for (int base = 0; base < n2; base += kMaxActive) {
+    const int cnt = min(kMaxActive, n2 - base);
+    if (threadIdx.x < cnt) {
+      const int dg = static_cast<int>((st2.g0 + base + threadIdx.x) % st2.per_expert);
+      __threadfence();
+      const bool last = atomicAdd(p.done + dg, 1u) == static_cast<unsigned>(n_active - 1);
+      __threadfence();
+      sh.last[threadIdx.x] = last ? dg : -1;
+    }
+    __syncthreads();
+    const int per = p.T * 16;
+    for (int i = threadIdx.x; i < cnt * per; i += kThreads) {
+      const int dg = sh.last[i / per];
+      if (dg < 0) continue;
+      const int t = (i % per) / 16, d0 = dg * 16 + i % 16;
+      float v = 0.0f;
+      for (int j = 0; j < p.k; ++j) v += __ldcg(p.o + static_cast<int64_t>(t * p.k + j) * p.D + d0);
+      p.y[static_cast<int64_t>(t) * p.D + d0] = float_to_bf16_bits(v);
+    }
+    __syncthreads();
+  }
+}
+
+template <int kFmt, int kN>
+moe_status_t launch(FewParams p, cudaStream_t s) {
+  const int fixed = p.T * p.row_pitch + (kN == 1 ? 2 : 1) * kWarps * 128 * kN * 4;
+  int stages = (kMaxSmem - 1024 * 4 - fixed) / (kWarps * slot_bytes<kFmt>());
+  if (stages > kMaxStages) stages = kMaxStages;
+  if (stages < 2) return MOE_ERR_UNSUPPORTED;
+  p.stages = stages;
+  const int smem = fixed + stages * kWarps * slot_bytes<kFmt>();
+  if (cudaFuncSetAttribute(few_kernel<kFmt, kN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  void* args[] = {&p};
+  if (cudaLaunchCooperativeKernel(reinterpret_cast<void*>(few_kernel<kFmt, kN>), dim3(num_sms()), dim3(kThreads), args,
+                                  smem, s) != cudaSuccess) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
+}
+
+}  // namespace
+
+int few_max_tokens(const moe_dims_t& d) {
+  const int64_t wide = d.D > d.I ? d.D : d.I;
+  const int64_t t = kMaxRowBytes / (2 * wide);
+  return static_cast<int>(t < kMaxT ? t : kMaxT);
+}
+
+moe_status_t launch_few(const moe_dims_t& d, const uint16_t* x, const uint16_t* Wr, const uint16_t* br,
+                        const moe_weight_t& W1, const uint16_t* b1, const moe_weight_t& W2, const uint16_t* b2,
+                        uint16_t* y, float* logits, uint16_t* h, float* o, unsigned* done, void* ws, cudaStream_t s) {
+  FewParams p{};
+  p.T = d.T;
+  p.D = d.D;
+  p.E = d.E;
+  p.k = d.k;
+  p.I = d.I;
+  p.x = x;
+  p.Wr = Wr;
+  p.br = br;
+  p.b1 = b1;
+  p.b2 = b2;
+  p.w1 = static_cast<const uint8_t*>(W1.data);
+  p.w2 = static_cast<const uint8_t*>(W2.data);
+  p.s1 = W1.scales;
+  p.s2 = W2.scales;
+  p.logits = logits;
+  p.h = h;
+  p.o = o;
+  p.done = done;
+  p.y = y;
+  p.header = static_cast<unsigned*>(ws);
+  // rows 64 bytes off a multiple of 128: two rows' 64-byte pieces on distinct banks
+  p.row_pitch = (d.D > d.I ? d.D : d.I) * 2 + 64;
+  p.act = act_of(d);
+  if (d.wfmt == MOE_W_BF16)
+    return d.T <= 8 ? launch<MOE_W_BF16, 1>(p, s) : launch<MOE_W_BF16, 2>(p, s);
+  return d.T <= 8 ? launch<MOE_W_MXFP4, 1>(p, s) : launch<MOE_W_MXFP4, 2>(p, s);
+}
+
+}  // namespace moe

@@ -90,6 +90,7 @@ struct FewParams {
   uint16_t* y;
   unsigned* header;  // workspace header
   int stages;
+  int red_bufs;      // buffers for the warps' partial sums: 2, or 1 where shared memory is short
   int row_pitch;     // bytes between resident activation rows
   Act act;
 };
@@ -424,10 +425,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   // resident rows | partial sums | rings
   uint8_t* act = smem;
-  constexpr int kRedBufs = kN == 1 ? 2 : 1;
   float* red = reinterpret_cast<float*>(smem + p.T * p.row_pitch);
   constexpr int kRedFloats = kWarps * 128 * kN;
-  uint8_t* ring = reinterpret_cast<uint8_t*>(red + kRedBufs * kRedFloats);
+  uint8_t* ring = reinterpret_cast<uint8_t*>(red + p.red_bufs * kRedFloats);
   __shared__ FewShared sh;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
   };
   for (int i = 0; i < p.stages; ++i) issue();
 
-  int slot = 0, buf = 0;
+  int slot = 0, buf = 0, turn = 0;
   const uint32_t act_at = sm100::smem_u32(act);
 #pragma unroll 1
   for (int which = 1; which <= 2; ++which) {
@@ -565,6 +565,17 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
 #pragma unroll
       for (int i = 0; i < kN; ++i)  // a column without a token repeats the last row; its sums are not used
         brow[i] = static_cast<uint32_t>(min(8 * i + lane / 4, rows - 1)) * p.row_pitch;
+      // the 4 kN warps that finish this granule (they take turns), and what
+      // they need from memory, asked for before the multiplication
+      const int ew = (warp - turn * 4 * kN) & (kWarps - 1);
+      const int grp = ew / 4, at = (ew % 4) * 32 + lane;
+      // fragment element -> weight row r and token n
+      const int r = at / 16 + (at & 2 ? 8 : 0), n = 8 * grp + (at / 4 % 4) * 2 + (at & 1);
+      const bool on = ew < 4 * kN && n < rows;
+      uint16_t bias = 0;
+      if (on)
+        bias = which == 1 ? p.b1[static_cast<int64_t>(e) * 2 * p.I + local * 8 + (r < 8 ? r : p.I + r - 8)]
+                          : p.b2[static_cast<int64_t>(e) * p.D + local * 16 + r];
       float acc[kN][4];
 #pragma unroll
       for (int i = 0; i < kN; ++i)
@@ -585,33 +596,22 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
         *reinterpret_cast<float4*>(part + (warp * kN + i) * 128 + lane * 4) =
             make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
       __syncthreads();
-      if (warp < 4 * kN) {
-        const int grp = warp / 4, at = threadIdx.x & 127;
+      if (ew < 4 * kN) {
         float v = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) v += part[(w * kN + grp) * 128 + at];
-        // fragment element -> weight row and token
-        const int src = at / 4, c = at % 4;
-        const int r = src / 4 + (c >= 2 ? 8 : 0), n = 8 * grp + (src % 4) * 2 + (c & 1);
-        const bool on = n < rows;
         if (kFmt == MOE_W_MXFP4 && on) v *= sh.row_scale[n];
+        v += bf16_bits_to_float(bias);
         const int a = on ? sh.row[n] : 0;
         if (which == 1) {
-          const float upv = __shfl_xor_sync(0xffffffffu, v, 2);
-          if (on && c < 2) {
-            const int i0 = local * 8 + r;
-            const uint16_t* bias = p.b1 + static_cast<int64_t>(e) * 2 * p.I;
-            const float gate = v + bf16_bits_to_float(bias[i0]), up = upv + bf16_bits_to_float(bias[p.I + i0]);
-            p.h[static_cast<int64_t>(a) * p.I + i0] = float_to_bf16_bits(glu_act(gate, up, p.act));
-          }
+          const float up = __shfl_xor_sync(0xffffffffu, v, 2);
+          if (on && r < 8) p.h[static_cast<int64_t>(a) * p.I + local * 8 + r] = float_to_bf16_bits(glu_act(v, up, p.act));
         } else if (on) {
-          const int d0 = local * 16 + r;
-          const float wgt = sh.gate[a / p.k][a % p.k];
-          p.o[static_cast<int64_t>(a) * p.D + d0] =
-              wgt * (v + bf16_bits_to_float(p.b2[static_cast<int64_t>(e) * p.D + d0]));
+          p.o[static_cast<int64_t>(a) * p.D + local * 16 + r] = sh.gate[a / p.k][a % p.k] * v;
         }
       }
-      if (kRedBufs == 1)
+      if (++turn == 4 / kN) turn = 0;
+      if (p.red_bufs == 1)
         __syncthreads();  // one buffer: its readers are done before the next granule writes it
       else
         buf ^= 1;         // two: the next granule's barrier orders them
@@ -652,12 +652,15 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
 
 template <int kFmt, int kN>
 moe_status_t launch(FewParams p, cudaStream_t s) {
-  const int fixed = p.T * p.row_pitch + (kN == 1 ? 2 : 1) * kWarps * 128 * kN * 4;
-  int stages = (kMaxSmem - 1024 * 4 - fixed) / (kWarps * slot_bytes<kFmt>());
+  const int red = kWarps * 128 * kN * 4, slots = kWarps * slot_bytes<kFmt>();
+  const int room = kMaxSmem - 4096 - p.T * p.row_pitch;
+  p.red_bufs = room - 2 * red >= 2 * slots ? 2 : 1;
+  const int fixed = p.T * p.row_pitch + p.red_bufs * red;
+  int stages = (room - p.red_bufs * red) / slots;
   if (stages > kMaxStages) stages = kMaxStages;
   if (stages < 2) return MOE_ERR_UNSUPPORTED;
   p.stages = stages;
-  const int smem = fixed + stages * kWarps * slot_bytes<kFmt>();
+  const int smem = fixed + stages * slots;
   if (cudaFuncSetAttribute(few_kernel<kFmt, kN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return MOE_ERR_CUDA;
   void* args[] = {&p};

@@ -64,6 +64,7 @@ template <>
 struct Fmt<MOE_W_BF16> {
   static constexpr int kUnitBytes = 64;           // 32 bf16
   static constexpr int kUnits = 2;                // units per warp and stage: 128 bytes of a row
+  static constexpr int kUnitsOfMany = 2;          // where a warp's units take several stages
   static constexpr int kPitch = 128;              // 16-byte chunks swizzled by row parity
   static constexpr int kScalePitch = 0;
 };
@@ -71,6 +72,7 @@ template <>
 struct Fmt<MOE_W_MXFP4> {
   static constexpr int kUnitBytes = 16;           // 32 codes
   static constexpr int kUnits = 6;
+  static constexpr int kUnitsOfMany = 4;          // a multiple of 4 scale bytes
   static constexpr int kPitch = 112;              // odd multiple of 16: 8 rows on distinct banks
   static constexpr int kScalePitch = 12;          // aligned words covering kUnits scale bytes
 };
@@ -143,6 +145,14 @@ __device__ __forceinline__ void mma_bf16_16816(float (&c)[4], uint32_t a0, uint3
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same with f16 operands, and with a zero in place of C.
+__device__ __forceinline__ void mma_f16_16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                   uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -164,7 +174,7 @@ __device__ __forceinline__ void e2m1_to_f16(uint32_t codes, uint32_t (&p)[4]) {
 }
 
 // E8M0: 2^(s - 127), the smallest a subnormal.
-__device__ __forceinline__ float e8m0(uint32_t s) { return __uint_as_float(s ? s << 23 : 0x00400000u); }
+__device__ __forceinline__ float e8m0(uint32_t s) { return __uint_as_float(max(s << 23, 0x00400000u)); }
 
 // All blocks of the grid meet (the launch is cooperative, so all are
 // resident). The last to arrive resets the count, so the state is the same
@@ -220,9 +230,9 @@ struct FewShared {
 
 // One weight's granules as this block and warp see them.
 struct Stream {
-  const uint8_t *w, *s;
   int64_t row_bytes;     // of the weight
-  int srow_bytes;        // of its scales
+  int srow_bytes;        // of its scales (even; a granule's first row is a multiple of 8 rows into the tensor, so
+                         // a row's scale bytes lie at the same offset from a 4-byte boundary in every granule)
   int rows;              // weight rows per expert
   int up;                // row of the 9th weight row relative to the 1st (I: the up half; 8)
   int step;              // weight rows a granule advances by (8 or 16)
@@ -230,15 +240,13 @@ struct Stream {
   int u0, u1;            // this warp's units of 32 of the reduction
   int chunk;             // units per stage
   int nchunks;           // stages per granule
-  int64_t g0, g1;        // this block's granules, over the active experts
+  int g0, g1;            // this block's granules, over the active experts
 };
 
 template <int kFmt>
 __device__ __forceinline__ Stream make_stream(const FewParams& p, int which, int n_active, int warp) {
   Stream s;
   const int K = which == 1 ? p.D : p.I;
-  s.w = which == 1 ? p.w1 : p.w2;
-  s.s = which == 1 ? p.s1 : p.s2;
   s.row_bytes = static_cast<int64_t>(K / 32) * Fmt<kFmt>::kUnitBytes;
   s.srow_bytes = K / 32;
   s.rows = which == 1 ? 2 * p.I : p.D;
@@ -246,107 +254,130 @@ __device__ __forceinline__ Stream make_stream(const FewParams& p, int which, int
   s.step = which == 1 ? 8 : 16;
   s.per_expert = which == 1 ? p.I / 8 : p.D / 16;
   const int units = K / 32, per = (units + kWarps - 1) / kWarps;
-  s.nchunks = (per + Fmt<kFmt>::kUnits - 1) / Fmt<kFmt>::kUnits;
-  s.chunk = (per + s.nchunks - 1) / s.nchunks;
+  s.chunk = per <= Fmt<kFmt>::kUnits ? per : Fmt<kFmt>::kUnitsOfMany;
+  s.nchunks = (per + s.chunk - 1) / s.chunk;
   s.u0 = min(units, warp * per);
   s.u1 = min(units, s.u0 + per);
-  const int64_t n = static_cast<int64_t>(n_active) * s.per_expert;
-  s.g0 = n * blockIdx.x / gridDim.x;
-  s.g1 = n * (blockIdx.x + 1) / gridDim.x;
+  const int64_t n = static_cast<int64_t>(n_active) * s.per_expert;  // (at most 128 * 2048)
+  s.g0 = static_cast<int>(n * blockIdx.x / gridDim.x);
+  s.g1 = static_cast<int>(n * (blockIdx.x + 1) / gridDim.x);
   return s;
 }
 
-// Copy this warp's part of one stage (granule, chunk) into its ring slot.
+// The loading end of a warp's ring: where its next stage comes from, and
+// which 16-byte pieces (and 4-byte words of scales) each lane copies.
 template <int kFmt>
-__device__ __forceinline__ void load_stage(const Stream& st, int expert, int local, int chunk, uint32_t slot,
-                                           int lane) {
-  constexpr int kU = Fmt<kFmt>::kUnits;
-  constexpr int kRowChunks = kU * Fmt<kFmt>::kUnitBytes / 16;  // 16-byte chunks of a row
-  const int u = st.u0 + chunk * st.chunk;
-  const int n = min(st.chunk, st.u1 - u);
-  if (n <= 0) return;
-  const int64_t row0 = static_cast<int64_t>(expert) * st.rows + static_cast<int64_t>(local) * st.step;
-  const uint8_t* base = st.w + row0 * st.row_bytes + static_cast<int64_t>(u) * Fmt<kFmt>::kUnitBytes;
-  const int valid = n * Fmt<kFmt>::kUnitBytes / 16;
-#pragma unroll
-  for (int i = 0; i < 16 * kRowChunks / 32; ++i) {
-    const int idx = lane + 32 * i;
-    const int r = idx / kRowChunks, c = idx % kRowChunks;
-    if (c < valid) {
-      const int wr = r < 8 ? r : st.up + r - 8;
-      const int cc = kFmt == MOE_W_BF16 ? c ^ ((r & 1) << 2) : c;
-      cp_async16(slot + r * Fmt<kFmt>::kPitch + cc * 16, base + wr * st.row_bytes + c * 16);
-    }
-  }
-  if (kFmt == MOE_W_MXFP4) {
-    // the aligned 4-byte words that hold each row's scale bytes [u, u + n)
-    // (the tensor's size is a multiple of 4, so they lie inside it)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int idx = lane + 32 * i;
-      const int r = idx / 3, c = idx % 3;
-      if (r < 16) {
-        const int wr = r < 8 ? r : st.up + r - 8;
-        const int64_t at = (row0 + wr) * st.srow_bytes + u;
-        const int64_t first = at & ~int64_t(3);
-        if (first + 4 * c < at + n)
-          cp_async4(slot + 16 * Fmt<kFmt>::kPitch + r * Fmt<kFmt>::kScalePitch + 4 * c, st.s + first + 4 * c);
-      }
-    }
-  }
-}
+struct Loader {
+  static constexpr int kRowChunks = Fmt<kFmt>::kUnits * Fmt<kFmt>::kUnitBytes / 16;  // 16-byte pieces of a row
+  static constexpr int kPieces = 16 * kRowChunks / 32;
+  static constexpr int kWords = kFmt == MOE_W_MXFP4 ? 2 : 0;
+  uint32_t off[kPieces];        // from the granule's first row, this warp's first unit
+  uint32_t soff[kWords + 1];
+  const uint8_t *w, *s;         // the current granule's first row
+  int g, ai, local, chunk;
 
-// Multiply one landed stage: acc (kN groups of 8 tokens) += 16 weight rows x
-// the stage's units.
-template <int kFmt, int kN>
-__device__ __forceinline__ void mul_stage(const Stream& st, int expert, int local, int chunk, uint32_t slot,
-                                          uint32_t act, const uint32_t (&brow)[kN], int lane, float (&acc)[kN][4]) {
-  const int r = lane / 4, q = lane % 4;
-  const int u = st.u0 + chunk * st.chunk;
-  const int n = min(st.chunk, st.u1 - u);
-  if (n <= 0) return;
-  if (kFmt == MOE_W_BF16) {
-    // two units of a row are 8 chunks of 16 bytes: chunk 4*j + q, the halves
-    // exchanged in odd rows (conflict-free)
+  __device__ __forceinline__ void granule(const FewParams& p, const FewShared& sh, const Stream& st, int which) {
+    const int64_t row0 = static_cast<int64_t>(sh.expert[ai]) * st.rows + static_cast<int64_t>(local) * st.step;
+    w = (which == 1 ? p.w1 : p.w2) + row0 * st.row_bytes;
+    if (kFmt == MOE_W_MXFP4) s = (which == 1 ? p.s1 : p.s2) + row0 * st.srow_bytes;
+  }
+
+  __device__ __forceinline__ void start(const FewParams& p, const FewShared& sh, const Stream& st, int which,
+                                        int lane) {
+    g = st.g0;
+    ai = g / st.per_expert;
+    local = g % st.per_expert;
+    chunk = 0;
 #pragma unroll
-    for (int j = 0; j < Fmt<kFmt>::kUnits; ++j) {
-      if (j < n) {
-        const uint32_t off = static_cast<uint32_t>(((4 * j + q) ^ ((r & 1) << 2)) * 16);
-        const uint4 a = lds128(slot + r * Fmt<kFmt>::kPitch + off);
-        const uint4 a8 = lds128(slot + (r + 8) * Fmt<kFmt>::kPitch + off);
+    for (int i = 0; i < kPieces; ++i) {
+      const int idx = lane + 32 * i, r = idx / kRowChunks, c = idx % kRowChunks;
+      const int wr = r < 8 ? r : st.up + r - 8;
+      off[i] = static_cast<uint32_t>(wr * st.row_bytes + st.u0 * Fmt<kFmt>::kUnitBytes + c * 16);
+    }
 #pragma unroll
-        for (int g = 0; g < kN; ++g) {
-          const uint4 b = lds128(act + brow[g] + (u + j) * 64 + q * 16);
-          mma_bf16_16816(acc[g], a.x, a8.x, a.y, a8.y, b.x, b.y);
-          mma_bf16_16816(acc[g], a.z, a8.z, a.w, a8.w, b.z, b.w);
-        }
+    for (int i = 0; i < kWords; ++i) {
+      const int idx = lane + 32 * i, r = idx / 3, c = idx % 3;
+      const int wr = r < 8 ? r : st.up + r - 8;
+      soff[i] = ((static_cast<uint32_t>(wr) * st.srow_bytes + st.u0) & ~3u) + 4 * c;
+    }
+    if (g < st.g1) granule(p, sh, st, which);
+  }
+
+  // Copy this warp's part of the next stage into its ring slot.
+  __device__ __forceinline__ void load(const FewParams& p, const FewShared& sh, const Stream& st, int which,
+                                       uint32_t slot, int lane) {
+    const int u = chunk * st.chunk;  // from the warp's first unit
+    const int n = min(st.chunk, st.u1 - st.u0 - u);
+    const int valid = n * (Fmt<kFmt>::kUnitBytes / 16);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int idx = lane + 32 * i, r = idx / kRowChunks, c = idx % kRowChunks;
+      const int cc = kFmt == MOE_W_BF16 ? c ^ ((r & 1) << 2) : c;
+      if (c < valid)
+        cp_async16(slot + r * Fmt<kFmt>::kPitch + cc * 16, w + off[i] + u * Fmt<kFmt>::kUnitBytes);
+    }
+    if (kFmt == MOE_W_MXFP4) {
+      // the aligned words that hold the scale bytes of units [u, u + n): u is
+      // a multiple of 4 (the tensor's size too, so the words lie inside it)
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const int idx = lane + 32 * i, r = idx / 3, c = idx % 3;
+        const int wr = r < 8 ? r : st.up + r - 8;
+        const int lead = static_cast<int>((static_cast<uint32_t>(wr) * st.srow_bytes + st.u0) & 3u);
+        if (r < 16 && n > 0 && 4 * c < lead + n)
+          cp_async4(slot + 16 * Fmt<kFmt>::kPitch + r * Fmt<kFmt>::kScalePitch + 4 * c, s + soff[i] + u);
       }
     }
-  } else {
-    const int64_t row0 = static_cast<int64_t>(expert) * st.rows + static_cast<int64_t>(local) * st.step;
-    const uint32_t sl = slot + 16 * Fmt<kFmt>::kPitch;
-    const uint32_t s_lo = sl + r * Fmt<kFmt>::kScalePitch +
-                          static_cast<uint32_t>(((row0 + r) * st.srow_bytes + u) & 3);
-    const uint32_t s_hi = sl + (r + 8) * Fmt<kFmt>::kScalePitch +
-                          static_cast<uint32_t>(((row0 + st.up + r) * st.srow_bytes + u) & 3);
+    if (++chunk == st.nchunks) {
+      chunk = 0;
+      ++g;
+      if (++local == st.per_expert) {
+        local = 0;
+        ++ai;
+        if (g < st.g1) granule(p, sh, st, which);
+      } else {
+        w += st.step * st.row_bytes;
+        if (kFmt == MOE_W_MXFP4) s += st.step * st.srow_bytes;
+      }
+    }
+  }
+};
+
+// Multiply kUnits landed units: acc (kN groups of 8 tokens) += 16 weight rows
+// x the units. `a`: the lane's place in its row of the slot; `b`: in its rows
+// of the activations; `s_lo`, `s_hi`: of its rows' scales.
+template <int kFmt, int kN, int kUnits>
+__device__ __forceinline__ void mul_units(uint32_t slot, int r, int q, int j0, const uint32_t (&b)[kN], uint32_t s_lo,
+                                          uint32_t s_hi, float (&acc)[kN][4]) {
 #pragma unroll
-    for (int j = 0; j < Fmt<kFmt>::kUnits; ++j) {
-      if (j < n) {
-        uint32_t a[4], a8[4];
-        e2m1_to_f16(lds32(slot + r * Fmt<kFmt>::kPitch + j * 16 + q * 4), a);
-        e2m1_to_f16(lds32(slot + (r + 8) * Fmt<kFmt>::kPitch + j * 16 + q * 4), a8);
-        const float w_lo = e8m0(lds8(s_lo + j)), w_hi = e8m0(lds8(s_hi + j));
+  for (int j = 0; j < kUnits; ++j) {
+    if (kFmt == MOE_W_BF16) {
+      // two units of a row are 8 chunks of 16 bytes: chunk 4*j + q, the halves
+      // exchanged in odd rows (conflict-free)
+      const uint32_t at = slot + r * Fmt<kFmt>::kPitch + (((4 * (j0 + j) + q) ^ ((r & 1) << 2)) * 16);
+      const uint4 a = lds128(at), a8 = lds128(at + 8 * Fmt<kFmt>::kPitch);
 #pragma unroll
-        for (int g = 0; g < kN; ++g) {
-          const uint4 b = lds128(act + brow[g] + (u + j) * 64 + q * 16);
-          float c[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_f16_16816(c, a[0], a8[0], a[1], a8[1], b.x, b.y);
-          mma_f16_16816(c, a[2], a8[2], a[3], a8[3], b.z, b.w);
-          acc[g][0] = fmaf(w_lo, c[0], acc[g][0]);
-          acc[g][1] = fmaf(w_lo, c[1], acc[g][1]);
-          acc[g][2] = fmaf(w_hi, c[2], acc[g][2]);
-          acc[g][3] = fmaf(w_hi, c[3], acc[g][3]);
-        }
+      for (int g = 0; g < kN; ++g) {
+        const uint4 v = lds128(b[g] + j * 64);
+        mma_bf16_16816(acc[g], a.x, a8.x, a.y, a8.y, v.x, v.y);
+        mma_bf16_16816(acc[g], a.z, a8.z, a.w, a8.w, v.z, v.w);
+      }
+    } else {
+      const uint32_t at = slot + r * Fmt<kFmt>::kPitch + q * 4 + (j0 + j) * 16;
+      uint32_t a[4], a8[4];
+      e2m1_to_f16(lds32(at), a);
+      e2m1_to_f16(lds32(at + 8 * Fmt<kFmt>::kPitch), a8);
+      const float w_lo = e8m0(lds8(s_lo + j)), w_hi = e8m0(lds8(s_hi + j));
+#pragma unroll
+      for (int g = 0; g < kN; ++g) {
+        const uint4 v = lds128(b[g] + j * 64);
+        float c[4];
+        mma_f16_16816_zero(c, a[0], a8[0], a[1], a8[1], v.x, v.y);
+        mma_f16_16816(c, a[2], a8[2], a[3], a8[3], v.z, v.w);
+        acc[g][0] = fmaf(w_lo, c[0], acc[g][0]);
+        acc[g][1] = fmaf(w_lo, c[1], acc[g][1]);
+        acc[g][2] = fmaf(w_hi, c[2], acc[g][2]);
+        acc[g][3] = fmaf(w_hi, c[3], acc[g][3]);
       }
     }
   }
@@ -515,31 +546,16 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
   const Stream st1 = make_stream<kFmt>(p, 1, n_active, warp);
   const Stream st2 = make_stream<kFmt>(p, 2, n_active, warp);
   const uint32_t ring_at = sm100::smem_u32(ring) + warp * p.stages * slot_bytes<kFmt>();
-  // where the loads stand
-  int ld_phase = 1;
-  int64_t ld_g = st1.g0;
-  int ld_ai = static_cast<int>(ld_g / st1.per_expert), ld_local = static_cast<int>(ld_g % st1.per_expert), ld_chunk = 0;
-  int ld_slot = 0;
+  Loader<kFmt> ld;
+  ld.start(p, sh, st1, 1, lane);
+  int ld_which = 1, ld_slot = 0;
   auto issue = [&]() {
-    if (ld_phase == 1 && ld_g >= st1.g1) {
-      ld_phase = 2;
-      ld_g = st2.g0;
-      ld_ai = static_cast<int>(ld_g / st2.per_expert);
-      ld_local = static_cast<int>(ld_g % st2.per_expert);
-      ld_chunk = 0;
+    if (ld_which == 1 && ld.g >= st1.g1) {
+      ld_which = 2;
+      ld.start(p, sh, st2, 2, lane);
     }
-    const Stream& s = ld_phase == 1 ? st1 : st2;
-    if (ld_g < s.g1) {
-      load_stage<kFmt>(s, sh.expert[ld_ai], ld_local, ld_chunk, ring_at + ld_slot * slot_bytes<kFmt>(), lane);
-      if (++ld_chunk == s.nchunks) {
-        ld_chunk = 0;
-        ++ld_g;
-        if (++ld_local == s.per_expert) {
-          ld_local = 0;
-          ++ld_ai;
-        }
-      }
-    }
+    const Stream& st = ld_which == 1 ? st1 : st2;
+    if (ld.g < st.g1) ld.load(p, sh, st, ld_which, ring_at + ld_slot * slot_bytes<kFmt>(), lane);
     cp_commit();
     if (++ld_slot == p.stages) ld_slot = 0;
   };
@@ -551,9 +567,15 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
   for (int which = 1; which <= 2; ++which) {
     const Stream& s = which == 1 ? st1 : st2;
     if (which == 2) grid_barrier(p.header);  // h is complete
-    int ai = static_cast<int>(s.g0 / s.per_expert), local = static_cast<int>(s.g0 % s.per_expert);
+    int ai = s.g0 / s.per_expert, local = s.g0 % s.per_expert;
     bool fresh = true;
-    for (int64_t g = s.g0; g < s.g1; ++g) {
+    const int fr = lane / 4, fq = lane % 4;
+    // where the lane's two rows' scale bytes start in a slot
+    const uint32_t s_lo = 16 * Fmt<kFmt>::kPitch + fr * Fmt<kFmt>::kScalePitch +
+                          ((static_cast<uint32_t>(fr) * s.srow_bytes + s.u0) & 3u);
+    const uint32_t s_hi = 16 * Fmt<kFmt>::kPitch + (fr + 8) * Fmt<kFmt>::kScalePitch +
+                          ((static_cast<uint32_t>(s.up + fr) * s.srow_bytes + s.u0) & 3u);
+    for (int g = s.g0; g < s.g1; ++g) {
       if (fresh) {
         __syncthreads();  // the previous expert's rows are read no more
         load_rows<kFmt>(p, sh, which, ai, act);
@@ -564,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
       uint32_t brow[kN];
 #pragma unroll
       for (int i = 0; i < kN; ++i)  // a column without a token repeats the last row; its sums are not used
-        brow[i] = static_cast<uint32_t>(min(8 * i + lane / 4, rows - 1)) * p.row_pitch;
+        brow[i] = act_at + min(8 * i + fr, rows - 1) * p.row_pitch + s.u0 * 64 + fq * 16;
       // the 4 kN warps that finish this granule (they take turns), and what
       // they need from memory, asked for before the multiplication
       const int ew = (warp - turn * 4 * kN) & (kWarps - 1);
@@ -584,7 +606,20 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
       for (int chunk = 0; chunk < s.nchunks; ++chunk) {
         cp_wait_upto(p.stages - 1);
         __syncwarp();
-        mul_stage<kFmt, kN>(s, e, local, chunk, ring_at + slot * slot_bytes<kFmt>(), act_at, brow, lane, acc);
+        const uint32_t at_slot = ring_at + slot * slot_bytes<kFmt>();
+        const int u = chunk * s.chunk, n = min(s.chunk, s.u1 - s.u0 - u);
+        uint32_t b[kN];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) b[i] = brow[i] + u * 64;
+        if (n == Fmt<kFmt>::kUnits) {
+          mul_units<kFmt, kN, Fmt<kFmt>::kUnits>(at_slot, fr, fq, 0, b, at_slot + s_lo, at_slot + s_hi, acc);
+        } else {
+          for (int j = 0; j < n; ++j) {
+            mul_units<kFmt, kN, 1>(at_slot, fr, fq, j, b, at_slot + s_lo + j, at_slot + s_hi + j, acc);
+#pragma unroll
+            for (int i = 0; i < kN; ++i) b[i] += 64;
+          }
+        }
         __syncwarp();
         issue();
         if (++slot == p.stages) slot = 0;
@@ -626,11 +661,11 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
 
   // ---- combine: the block whose granule is the last of its 16 columns
   __syncthreads();
-  const int n2 = static_cast<int>(st2.g1 - st2.g0);
+  const int n2 = st2.g1 - st2.g0;
   for (int base = 0; base < n2; base += kMaxActive) {
     const int cnt = min(kMaxActive, n2 - base);
     if (threadIdx.x < cnt) {
-      const int dg = static_cast<int>((st2.g0 + base + threadIdx.x) % st2.per_expert);
+      const int dg = (st2.g0 + base + static_cast<int>(threadIdx.x)) % st2.per_expert;
       __threadfence();
       const bool last = atomicAdd(p.done + dg, 1u) == static_cast<unsigned>(n_active - 1);
       __threadfence();

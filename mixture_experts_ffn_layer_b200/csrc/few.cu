@@ -5,12 +5,13 @@
 // memory bound, and with eight launches between which nothing streams, latency
 // bound too. Here one cooperative kernel, one block per SM, does all of it:
 //
-//   1. router: one warp per (token, expert) logit, fp32 dot product;
-//      grid barrier; every block takes the top-k of all tokens itself (the
-//      same arithmetic everywhere) and lists the experts with rows.
+//   1. router: every block takes a few (token, expert) logits, fp32 dot
+//      products, and brings the tokens' rows into shared memory; grid barrier;
+//      every block takes the top-k of all tokens itself (the same arithmetic
+//      everywhere) and lists the experts with rows.
 //   2. mlp1: the active experts' hidden units, 8 at a time (a granule: 8 gate
 //      rows and the 8 up rows of W1), are split evenly over the blocks; h
-//      (bf16, by assignment) goes to the workspace; grid barrier.
+//      (bf16, rows by expert) goes to the workspace; grid barrier.
 //   3. mlp2: granules of 16 rows of W2, split the same way; the fp32 expert
 //      outputs go to the workspace, and the block that finishes the last
 //      expert of 16 output columns sums their k terms per token in slot order.
@@ -27,7 +28,9 @@
 // loaded -- and the tensor rate is far from being a limit. The k index of an
 // MMA is permuted (lane q of a row's four holds 8 consecutive elements of a
 // 32-element unit), the same for weights and activations, so both are read
-// with wide shared-memory loads.
+// with wide shared-memory loads. The warps' partial sums meet in shared memory
+// behind mbarriers (full / empty per buffer): a few warps, taking turns, add
+// them in warp order and finish the granule while the others go on.
 //
 // MXFP4: a unit of 32 codes is one scale block. The codes become f16 (exact),
 // the activations f16 with one power of two per row such that the largest
@@ -52,11 +55,14 @@ constexpr int kMaxK = 8;
 constexpr int kMaxActive = kMaxT * kMaxK;
 constexpr int kMaxSmem = 232448;      // 227 KB per block
 constexpr int kMaxStages = 8;
+constexpr int kMaxBufs = 4;
 constexpr int64_t kMaxRowBytes = 65536 * 2;  // T * max(D, I) bf16 of resident activations
 constexpr uint64_t kBarrierNs = 1000000000ull;
 
-// Grid-barrier state in the workspace header (the status word is at byte 0).
-constexpr int kBarCount = 16, kBarGen = 17;  // as 32-bit words
+// Grid-barrier counters in the workspace header (the status word is at byte
+// 0), as 32-bit words: blocks that reached the first and the second barrier,
+// and blocks that are done.
+constexpr int kBar1 = 16, kBar2 = 24, kExit = 32;
 
 template <int kFmt>
 struct Fmt;
@@ -86,13 +92,13 @@ struct FewParams {
   const uint16_t *x, *Wr, *br, *b1, *b2;
   const uint8_t *w1, *w2, *s1, *s2;
   float* logits;     // (T, E)
-  uint16_t* h;       // (T*k, I) bf16, by assignment
+  uint16_t* h;       // (T*k, I) bf16, rows by expert
   float* o;          // (T*k, D) fp32, by assignment, gate weight applied
   unsigned* done;    // (D/16) expert granules finished
   uint16_t* y;
   unsigned* header;  // workspace header
   int stages;
-  int red_bufs;      // buffers for the warps' partial sums: 2, or 1 where shared memory is short
+  int red_bufs;      // buffers for the warps' partial sums: 4, or 2 or 1 where shared memory is short
   int row_pitch;     // bytes between resident activation rows
   Act act;
 };
@@ -173,36 +179,49 @@ __device__ __forceinline__ void e2m1_to_f16(uint32_t codes, uint32_t (&p)[4]) {
       : "r"(codes));
 }
 
-// E8M0: 2^(s - 127), the smallest a subnormal.
-__device__ __forceinline__ float e8m0(uint32_t s) { return __uint_as_float(max(s << 23, 0x00400000u)); }
+// E8M0: 2^(s - 127); the smallest, 2^-127, counts as zero.
+__device__ __forceinline__ float e8m0(uint32_t s) { return __uint_as_float(s << 23); }
 
 // All blocks of the grid meet (the launch is cooperative, so all are
-// resident). The last to arrive resets the count, so the state is the same
-// after every barrier. Waits at most kBarrierNs, then records the timeout and
-// goes on: every index computed later is in range whatever the data hold.
-__device__ __forceinline__ void grid_barrier(unsigned* header) {
+// resident). Waits at most kBarrierNs, then records the timeout and goes on:
+// every index computed later is in range whatever the data hold.
+__device__ __forceinline__ void grid_barrier(unsigned* header, int which) {
   __syncthreads();
   if (threadIdx.x == 0) {
-    __threadfence();
-    volatile unsigned* gen = header + kBarGen;
-    const unsigned g = *gen;
-    __threadfence();
-    if (atomicAdd(header + kBarCount, 1u) == gridDim.x - 1) {
-      atomicExch(header + kBarCount, 0u);
-      __threadfence();
-      atomicAdd(header + kBarGen, 1u);
-    } else {
-      const uint64_t t0 = sm100::globaltimer_ns();
-      for (uint32_t i = 1; *gen == g; ++i) {
-        if ((i & 255u) == 0 && sm100::globaltimer_ns() - t0 > kBarrierNs) {
+    unsigned* count = header + which;
+    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(count) : "memory");
+    unsigned seen;
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(count) : "memory");
+      if (seen >= gridDim.x) break;
+      if ((i & 63u) == 0) {
+        const uint64_t now = sm100::globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > kBarrierNs) {
           record_status(reinterpret_cast<int*>(header), MOE_ERR_TIMEOUT);
           break;
         }
       }
     }
-    __threadfence();
   }
   __syncthreads();
+}
+
+// The last block to leave sets the counters back to zero for the next call
+// (every block has then passed both barriers, or given up on them).
+__device__ __forceinline__ void grid_exit(unsigned* header) {
+  if (threadIdx.x == 0 && atomicAdd(header + kExit, 1u) == gridDim.x - 1) {
+    header[kBar1] = 0;
+    header[kBar2] = 0;
+    header[kExit] = 0;
+  }
+}
+
+// Wait inside the block for warps that are on their way.
+__device__ __forceinline__ void wait_local(uint32_t bar, uint32_t parity, unsigned* header) {
+  if (!sm100::mbar_wait_bounded(bar, parity, nullptr, kBarrierNs))
+    record_status(reinterpret_cast<int*>(header), MOE_ERR_TIMEOUT);
 }
 
 // Order-preserving integer of a logit; NaN sorts below every number, -0 as +0.
@@ -217,14 +236,18 @@ __device__ __forceinline__ float key_value(uint32_t key) {
 }
 
 struct FewShared {
+  uint64_t full[kMaxBufs], empty[kMaxBufs];  // of the partial-sum buffers
   int n_active;
-  uint16_t expert[kMaxActive];   // active experts, ascending
-  uint16_t tokens[kMaxActive];   // their tokens, a bit each
-  int16_t top[kMaxT][kMaxK];     // expert of each assignment
+  uint32_t tokens[256];          // per expert: its tokens, a bit each
+  uint8_t place[256];            // per expert: its place among the active ones
+  uint8_t expert[kMaxActive];    // active experts, ascending
+  uint8_t start[kMaxActive + 1]; // first row of each active expert
+  uint8_t slot[kMaxActive];      // per row: its assignment t * k + j
+  uint8_t top[kMaxT][kMaxK];     // expert of each assignment
   float gate[kMaxT][kMaxK];
-  int row[kMaxT];                // current expert: assignment of each resident row
+  float dot[kWarps];
   uint32_t row_max[kMaxT];       // |largest| of each resident row (bf16 bits)
-  float row_scale[kMaxT];        // what a row's sums are multiplied with
+  float row_scale[kMaxT];        // what a resident row's sums are multiplied with
   int last[kMaxActive];
 };
 
@@ -258,7 +281,7 @@ __device__ __forceinline__ Stream make_stream(const FewParams& p, int which, int
   s.nchunks = (per + s.chunk - 1) / s.chunk;
   s.u0 = min(units, warp * per);
   s.u1 = min(units, s.u0 + per);
-  const int64_t n = static_cast<int64_t>(n_active) * s.per_expert;  // (at most 128 * 2048)
+  const uint32_t n = n_active * s.per_expert;  // at most 128 * 2048
   s.g0 = static_cast<int>(n * blockIdx.x / gridDim.x);
   s.g1 = static_cast<int>(n * (blockIdx.x + 1) / gridDim.x);
   return s;
@@ -383,22 +406,12 @@ __device__ __forceinline__ void mul_units(uint32_t slot, int r, int q, int j0, c
   }
 }
 
-// Bring the rows of active expert `ai` into shared memory: x[t] (mlp1) or
-// h[a] (mlp2). MXFP4 rows become f16 scaled by a power of two.
+// Bring `rows` rows of K bf16 into shared memory; MXFP4 rows become f16
+// scaled by a power of two. row_max is zero on entry, and the block
+// synchronises before it reads the rows.
 template <int kFmt>
-__device__ __forceinline__ void load_rows(const FewParams& p, FewShared& sh, int which, int ai, uint8_t* act) {
-  const int K = which == 1 ? p.D : p.I;
-  const int e = sh.expert[ai];
-  const uint32_t tokens = sh.tokens[ai];
-  const int rows = __popc(tokens);
-  if (threadIdx.x < rows) {
-    const int t = __fns(tokens, 0, threadIdx.x + 1);
-    int j = 0;
-    while (j < p.k - 1 && sh.top[t][j] != e) ++j;
-    sh.row[threadIdx.x] = t * p.k + j;
-    sh.row_max[threadIdx.x] = 0;
-  }
-  __syncthreads();
+__device__ __forceinline__ void load_rows(const FewParams& p, FewShared& sh, const uint16_t* from, int rows, int K,
+                                          uint8_t* act) {
   const int per = K / 8;  // 16-byte chunks per row
   const int total = rows * per;
   for (int base = threadIdx.x & ~31; base < total; base += kThreads) {  // (uniform in a warp)
@@ -407,10 +420,7 @@ __device__ __forceinline__ void load_rows(const FewParams& p, FewShared& sh, int
     const int n = min(i, total - 1) / per, c = i - n * per;
     uint32_t m = 0;
     if (on) {
-      const int a = sh.row[n];
-      const uint4* src = reinterpret_cast<const uint4*>(which == 1 ? p.x + static_cast<int64_t>(a / p.k) * K
-                                                                   : p.h + static_cast<int64_t>(a) * K) + c;
-      const uint4 v = __ldcg(src);
+      const uint4 v = __ldcg(reinterpret_cast<const uint4*>(from) + i);
       *reinterpret_cast<uint4*>(act + n * p.row_pitch + c * 16) = v;
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -426,8 +436,8 @@ __device__ __forceinline__ void load_rows(const FewParams& p, FewShared& sh, int
       }
     }
   }
-  __syncthreads();
   if (kFmt == MOE_W_MXFP4) {
+    __syncthreads();
     for (int i = threadIdx.x; i < total; i += kThreads) {
       const int n = i / per, c = i - n * per;
       // 2^shift brings the row's largest magnitude into [2^8, 2^9); a row of
@@ -447,8 +457,13 @@ __device__ __forceinline__ void load_rows(const FewParams& p, FewShared& sh, int
       }
       *at = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    __syncthreads();
   }
+}
+
+// The n-th set bit of a mask (n below its number of bits).
+__device__ __forceinline__ int nth_bit(uint32_t mask, int n) {
+  for (; n > 0; --n) mask &= mask - 1;
+  return __ffs(mask) - 1;
 }
 
 template <int kFmt, int kN>
@@ -461,30 +476,63 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
   uint8_t* ring = reinterpret_cast<uint8_t*>(red + p.red_bufs * kRedFloats);
   __shared__ FewShared sh;
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // (the shuffle tells the compiler that the warp index is uniform)
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0), lane = threadIdx.x % 32;
 
-  // ---- router logits, one warp each; the completion counters start at zero
+  // ---- router logits; the tokens' rows; the completion counters start at zero
+  if (threadIdx.x < 256) sh.tokens[threadIdx.x] = 0;
+  if (threadIdx.x < kMaxT) sh.row_max[threadIdx.x] = 0;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kMaxBufs; ++i) {
+      sm100::mbar_init(sm100::smem_u32(&sh.full[i]), kWarps);
+      sm100::mbar_init(sm100::smem_u32(&sh.empty[i]), 4 * kN);
+    }
+    sm100::fence_mbar_init();
+  }
   for (int i = blockIdx.x * kThreads + threadIdx.x; i < p.D / 16; i += gridDim.x * kThreads) p.done[i] = 0;
-  for (int item = blockIdx.x * kWarps + warp; item < p.T * p.E; item += gridDim.x * kWarps) {
-    const int t = item / p.E, e = item - t * p.E;
-    const uint4* xr = reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(t) * p.D);
-    const uint4* wr = reinterpret_cast<const uint4*>(p.Wr + static_cast<int64_t>(e) * p.D);
-    float sum = 0.0f;
+  {
+    // this block's logits, each by 16 / groups warps (one warp when there are
+    // many), their parts added in warp order
+    const uint32_t items = p.T * p.E;
+    const int i0 = static_cast<int>(items * blockIdx.x / gridDim.x);
+    const int n = static_cast<int>(items * (blockIdx.x + 1) / gridDim.x) - i0;
+    int groups = 1;
+    while (groups < n && groups < kWarps) groups *= 2;
+    const int parts = kWarps / groups, part = warp % parts;
+    for (int i = warp / parts; i < n; i += groups) {
+      const int t = (i0 + i) / p.E, e = (i0 + i) % p.E;
+      const uint4* xr = reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(t) * p.D);
+      const uint4* wr = reinterpret_cast<const uint4*>(p.Wr + static_cast<int64_t>(e) * p.D);
+      float sum = 0.0f;
 #pragma unroll 6
-    for (int c = lane; c < p.D / 8; c += 32) {
-      const uint4 a = __ldg(xr + c), b = __ldg(wr + c);
-      const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+      for (int c = part * 32 + lane; c < p.D / 8; c += parts * 32) {
+        const uint4 a = __ldg(xr + c), b = __ldg(wr + c);
+        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-      for (int z = 0; z < 4; ++z) {
-        sum = fmaf(__uint_as_float(aw[z] << 16), __uint_as_float(bw[z] << 16), sum);
-        sum = fmaf(__uint_as_float(aw[z] & 0xffff0000u), __uint_as_float(bw[z] & 0xffff0000u), sum);
+        for (int z = 0; z < 4; ++z) {
+          sum = fmaf(__uint_as_float(aw[z] << 16), __uint_as_float(bw[z] << 16), sum);
+          sum = fmaf(__uint_as_float(aw[z] & 0xffff0000u), __uint_as_float(bw[z] & 0xffff0000u), sum);
+        }
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      if (lane == 0) {
+        if (parts == 1)
+          p.logits[i0 + i] = sum + bf16_bits_to_float(p.br[e]);
+        else
+          sh.dot[warp] = sum;
       }
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (lane == 0) p.logits[item] = sum + bf16_bits_to_float(p.br[e]);
+    __syncthreads();
+    if (parts > 1 && static_cast<int>(threadIdx.x) < n) {  // (then every logit had its own group)
+      float sum = 0.0f;
+      for (int i = 0; i < parts; ++i) sum += sh.dot[threadIdx.x * parts + i];
+      const int at = i0 + threadIdx.x;
+      p.logits[at] = sum + bf16_bits_to_float(p.br[at % p.E]);
+    }
   }
-  grid_barrier(p.header);
+  load_rows<kFmt>(p, sh, p.x, p.T, p.D, act);
+  grid_barrier(p.header, kBar1);
 
   // ---- top-k of every token (warp t), then the active experts
   if (warp < p.T) {
@@ -514,32 +562,44 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
       total += ex;
       if (lane == j) {
         mine = ex;
-        sh.top[warp][j] = static_cast<int16_t>(at);
+        sh.top[warp][j] = static_cast<uint8_t>(at);
+        atomicOr(&sh.tokens[at], 1u << warp);
       }
     }
     if (lane < p.k) sh.gate[warp][lane] = __fdividef(mine, total);
   }
   __syncthreads();
   if (warp == 0) {
-    // experts 32 i + lane: their tokens, and their place among the active ones
-    int n = 0;
+    int n = 0, rows = 0;  // active experts and rows before expert 32 i
     for (int base = 0; base < p.E; base += 32) {
       const int e = base + lane;
-      uint32_t tokens = 0;
-      for (int t = 0; t < p.T; ++t)
-        for (int j = 0; j < p.k; ++j)
-          if (sh.top[t][j] == e) tokens |= 1u << t;
-      const uint32_t has = __ballot_sync(0xffffffffu, tokens != 0);
-      if (tokens) {
+      const int mine = __popc(sh.tokens[e]);
+      int incl = mine;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += v;
+      }
+      const uint32_t has = __ballot_sync(0xffffffffu, mine != 0);
+      if (mine) {
         const int at = n + __popc(has & ((1u << lane) - 1u));
-        sh.expert[at] = static_cast<uint16_t>(e);
-        sh.tokens[at] = static_cast<uint16_t>(tokens);
+        sh.place[e] = static_cast<uint8_t>(at);
+        sh.expert[at] = static_cast<uint8_t>(e);
+        sh.start[at] = static_cast<uint8_t>(rows + incl - mine);
       }
       n += __popc(has);
+      rows += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) sh.n_active = n;
+    if (lane == 0) {
+      sh.n_active = n;
+      sh.start[n] = static_cast<uint8_t>(rows);
+    }
   }
   __syncthreads();
+  if (static_cast<int>(threadIdx.x) < p.T * p.k) {
+    const int t = threadIdx.x / p.k, e = sh.top[t][threadIdx.x % p.k];
+    sh.slot[sh.start[sh.place[e]] + __popc(sh.tokens[e] & ((1u << t) - 1u))] = static_cast<uint8_t>(threadIdx.x);
+  }
   const int n_active = sh.n_active;
 
   // ---- the weight stream: mlp1's stages, then mlp2's, through this warp's ring
@@ -560,36 +620,49 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
     if (++ld_slot == p.stages) ld_slot = 0;
   };
   for (int i = 0; i < p.stages; ++i) issue();
+  __syncthreads();  // the lists are complete
 
-  int slot = 0, buf = 0, turn = 0;
-  const uint32_t act_at = sm100::smem_u32(act);
+  int slot = 0, it = 0;
+  const int buf_shift = p.red_bufs >> 1;  // log2 of 1, 2 or 4
+  const uint32_t act_at = sm100::smem_u32(act), red_at = sm100::smem_u32(red);
+  const uint32_t full_at = sm100::smem_u32(sh.full), empty_at = sm100::smem_u32(sh.empty);
+  const int fr = lane / 4, fq = lane % 4;
 #pragma unroll 1
   for (int which = 1; which <= 2; ++which) {
     const Stream& s = which == 1 ? st1 : st2;
-    if (which == 2) grid_barrier(p.header);  // h is complete
+    if (which == 2) grid_barrier(p.header, kBar2);  // h is complete
     int ai = s.g0 / s.per_expert, local = s.g0 % s.per_expert;
     bool fresh = true;
-    const int fr = lane / 4, fq = lane % 4;
     // where the lane's two rows' scale bytes start in a slot
     const uint32_t s_lo = 16 * Fmt<kFmt>::kPitch + fr * Fmt<kFmt>::kScalePitch +
                           ((static_cast<uint32_t>(fr) * s.srow_bytes + s.u0) & 3u);
     const uint32_t s_hi = 16 * Fmt<kFmt>::kPitch + (fr + 8) * Fmt<kFmt>::kScalePitch +
                           ((static_cast<uint32_t>(s.up + fr) * s.srow_bytes + s.u0) & 3u);
-    for (int g = s.g0; g < s.g1; ++g) {
+    int e = 0, rows = 0, start = 0;
+    uint32_t brow[kN];
+    for (int g = s.g0; g < s.g1; ++g, ++it) {
       if (fresh) {
-        __syncthreads();  // the previous expert's rows are read no more
-        load_rows<kFmt>(p, sh, which, ai, act);
         fresh = false;
-      }
-      const int rows = __popc(static_cast<uint32_t>(sh.tokens[ai]));
-      const int e = sh.expert[ai];
-      uint32_t brow[kN];
+        e = sh.expert[ai];
+        start = sh.start[ai];
+        rows = sh.start[ai + 1] - start;
+        if (which == 2) {
+          __syncthreads();  // the previous expert's rows are read no more
+          if (threadIdx.x < kMaxT) sh.row_max[threadIdx.x] = 0;
+          __syncthreads();
+          load_rows<kFmt>(p, sh, p.h + static_cast<int64_t>(start) * p.I, rows, p.I, act);
+          __syncthreads();
+        }
+        // a column without a token repeats the last row; its sums are not used
 #pragma unroll
-      for (int i = 0; i < kN; ++i)  // a column without a token repeats the last row; its sums are not used
-        brow[i] = act_at + min(8 * i + fr, rows - 1) * p.row_pitch + s.u0 * 64 + fq * 16;
+        for (int i = 0; i < kN; ++i) {
+          const int n = min(8 * i + fr, rows - 1);
+          brow[i] = act_at + (which == 1 ? nth_bit(sh.tokens[e], n) : n) * p.row_pitch + s.u0 * 64 + fq * 16;
+        }
+      }
       // the 4 kN warps that finish this granule (they take turns), and what
       // they need from memory, asked for before the multiplication
-      const int ew = (warp - turn * 4 * kN) & (kWarps - 1);
+      const int ew = (warp - it * 4 * kN) & (kWarps - 1);
       const int grp = ew / 4, at = (ew % 4) * 32 + lane;
       // fragment element -> weight row r and token n
       const int r = at / 16 + (at & 2 ? 8 : 0), n = 8 * grp + (at / 4 % 4) * 2 + (at & 1);
@@ -624,32 +697,37 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
         issue();
         if (++slot == p.stages) slot = 0;
       }
-      // sum the 16 warps' parts in warp order
-      float* part = red + buf * kRedFloats;
+      // the 16 warps' parts meet in buffer it mod red_bufs
+      const int buf = it & (p.red_bufs - 1), round = it >> buf_shift;
+      const uint32_t part = red_at + buf * (kRedFloats * 4);
+      if (round > 0) wait_local(empty_at + 8 * buf, (round - 1) & 1, p.header);
 #pragma unroll
       for (int i = 0; i < kN; ++i)
-        *reinterpret_cast<float4*>(part + (warp * kN + i) * 128 + lane * 4) =
-            make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-      __syncthreads();
+        sm100::st_shared_v4(part + ((warp * kN + i) * 128 + lane * 4) * 4, __float_as_uint(acc[i][0]),
+                            __float_as_uint(acc[i][1]), __float_as_uint(acc[i][2]), __float_as_uint(acc[i][3]));
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(full_at + 8 * buf);
       if (ew < 4 * kN) {
+        wait_local(full_at + 8 * buf, round & 1, p.header);
         float v = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) v += part[(w * kN + grp) * 128 + at];
-        if (kFmt == MOE_W_MXFP4 && on) v *= sh.row_scale[n];
+        for (int w = 0; w < kWarps; ++w)
+          v += __uint_as_float(lds32(part + ((w * kN + grp) * 128 + at) * 4));
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(empty_at + 8 * buf);
+        const int row = start + n;
+        if (kFmt == MOE_W_MXFP4 && on)
+          v *= sh.row_scale[which == 1 ? sh.slot[row] / static_cast<uint32_t>(p.k) : n];
         v += bf16_bits_to_float(bias);
-        const int a = on ? sh.row[n] : 0;
         if (which == 1) {
           const float up = __shfl_xor_sync(0xffffffffu, v, 2);
-          if (on && r < 8) p.h[static_cast<int64_t>(a) * p.I + local * 8 + r] = float_to_bf16_bits(glu_act(v, up, p.act));
+          if (on && r < 8)
+            p.h[static_cast<int64_t>(row) * p.I + local * 8 + r] = float_to_bf16_bits(glu_act(v, up, p.act));
         } else if (on) {
+          const uint32_t a = sh.slot[row];
           p.o[static_cast<int64_t>(a) * p.D + local * 16 + r] = sh.gate[a / p.k][a % p.k] * v;
         }
       }
-      if (++turn == 4 / kN) turn = 0;
-      if (p.red_bufs == 1)
-        __syncthreads();  // one buffer: its readers are done before the next granule writes it
-      else
-        buf ^= 1;         // two: the next granule's barrier orders them
       if (++local == s.per_expert) {
         local = 0;
         ++ai;
@@ -664,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
   const int n2 = st2.g1 - st2.g0;
   for (int base = 0; base < n2; base += kMaxActive) {
     const int cnt = min(kMaxActive, n2 - base);
-    if (threadIdx.x < cnt) {
+    if (static_cast<int>(threadIdx.x) < cnt) {
       const int dg = (st2.g0 + base + static_cast<int>(threadIdx.x)) % st2.per_expert;
       __threadfence();
       const bool last = atomicAdd(p.done + dg, 1u) == static_cast<unsigned>(n_active - 1);
@@ -683,13 +761,15 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
     }
     __syncthreads();
   }
+  grid_exit(p.header);
 }
 
 template <int kFmt, int kN>
 moe_status_t launch(FewParams p, cudaStream_t s) {
   const int red = kWarps * 128 * kN * 4, slots = kWarps * slot_bytes<kFmt>();
   const int room = kMaxSmem - 4096 - p.T * p.row_pitch;
-  p.red_bufs = room - 2 * red >= 2 * slots ? 2 : 1;
+  // the partial sums' buffers after two stages, then as many stages as fit
+  p.red_bufs = kN == 1 && room - 4 * red >= 2 * slots ? 4 : room - 2 * red >= 2 * slots ? 2 : 1;
   const int fixed = p.T * p.row_pitch + p.red_bufs * red;
   int stages = (room - p.red_bufs * red) / slots;
   if (stages > kMaxStages) stages = kMaxStages;

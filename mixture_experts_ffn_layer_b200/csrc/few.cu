@@ -70,16 +70,14 @@ template <>
 struct Fmt<MOE_W_BF16> {
   static constexpr int kUnitBytes = 64;           // 32 bf16
   static constexpr int kUnits = 2;                // units per warp and stage: 128 bytes of a row
-  static constexpr int kUnitsOfMany = 2;          // where a warp's units take several stages
   static constexpr int kPitch = 128;              // 16-byte chunks swizzled by row parity
   static constexpr int kScalePitch = 0;
 };
 template <>
 struct Fmt<MOE_W_MXFP4> {
   static constexpr int kUnitBytes = 16;           // 32 codes
-  static constexpr int kUnits = 6;
-  static constexpr int kUnitsOfMany = 4;          // a multiple of 4 scale bytes
-  static constexpr int kPitch = 112;              // odd multiple of 16: 8 rows on distinct banks
+  static constexpr int kUnits = 8;                // (a multiple of 4 scale bytes)
+  static constexpr int kPitch = 144;              // odd multiple of 16: 8 rows on distinct banks
   static constexpr int kScalePitch = 12;          // aligned words covering kUnits scale bytes
 };
 template <int kFmt>
@@ -251,6 +249,15 @@ struct FewShared {
   int last[kMaxActive];
 };
 
+// How many granules a block works on at a time, 16 / that many warps on each:
+// the more, the fewer partial sums meet and the longer each warp's slice; but
+// a block with few granules, or a short reduction, has too little for it.
+__device__ __forceinline__ int pick_sides(int granules, int units) {
+  int sides = 1;
+  while (sides < 4 && granules >= 4 * sides) sides *= 2;
+  return sides;
+}
+
 // One weight's granules as this block and warp see them.
 struct Stream {
   int64_t row_bytes;     // of the weight
@@ -260,8 +267,8 @@ struct Stream {
   int up;                // row of the 9th weight row relative to the 1st (I: the up half; 8)
   int step;              // weight rows a granule advances by (8 or 16)
   int per_expert;        // granules per expert
+  int side, sides;       // this warp's granule of the `sides` that the block works on at a time
   int u0, u1;            // this warp's units of 32 of the reduction
-  int chunk;             // units per stage
   int nchunks;           // stages per granule
   int g0, g1;            // this block's granules, over the active experts
 };
@@ -276,19 +283,19 @@ __device__ __forceinline__ Stream make_stream(const FewParams& p, int which, int
   s.up = which == 1 ? p.I : 8;
   s.step = which == 1 ? 8 : 16;
   s.per_expert = which == 1 ? p.I / 8 : p.D / 16;
-  const int units = K / 32, per = (units + kWarps - 1) / kWarps;
-  s.chunk = per <= Fmt<kFmt>::kUnits ? per : Fmt<kFmt>::kUnitsOfMany;
-  s.nchunks = (per + s.chunk - 1) / s.chunk;
-  s.u0 = min(units, warp * per);
-  s.u1 = min(units, s.u0 + per);
   const uint32_t n = n_active * s.per_expert;  // at most 128 * 2048
   s.g0 = static_cast<int>(n * blockIdx.x / gridDim.x);
   s.g1 = static_cast<int>(n * (blockIdx.x + 1) / gridDim.x);
+  s.sides = pick_sides(n / gridDim.x, K / 32);
+  const int split = kWarps / s.sides;
+  s.side = warp / split;
+  const int units = K / 32, per = (units + split - 1) / split;
+  s.nchunks = (per + Fmt<kFmt>::kUnits - 1) / Fmt<kFmt>::kUnits;
+  s.u0 = min(units, warp % split * per);
+  s.u1 = min(units, s.u0 + per);
   return s;
 }
 
-// The loading end of a warp's ring: where its next stage comes from, and
-// which 16-byte pieces (and 4-byte words of scales) each lane copies.
 template <int kFmt>
 struct Loader {
   static constexpr int kRowChunks = Fmt<kFmt>::kUnits * Fmt<kFmt>::kUnitBytes / 16;  // 16-byte pieces of a row
@@ -297,9 +304,20 @@ struct Loader {
   uint32_t off[kPieces];        // from the granule's first row, this warp's first unit
   uint32_t soff[kWords + 1];
   const uint8_t *w, *s;         // the current granule's first row
-  int g, ai, local, chunk;
+  int ai, local, end, chunk;    // active expert (-1: no more), granule, end of the expert's granules, stage
 
-  __device__ __forceinline__ void granule(const FewParams& p, const FewShared& sh, const Stream& st, int which) {
+  // To the warp's first granule from `ai` on, whose granules begin at `begin`.
+  __device__ __forceinline__ void seek(const FewParams& p, const FewShared& sh, const Stream& st, int which,
+                                       int begin) {
+    for (;; ++ai, begin = 0) {
+      if (ai * st.per_expert >= st.g1) {
+        ai = -1;
+        return;
+      }
+      end = min(st.per_expert, st.g1 - ai * st.per_expert);
+      local = begin + st.side;
+      if (local < end) break;
+    }
     const int64_t row0 = static_cast<int64_t>(sh.expert[ai]) * st.rows + static_cast<int64_t>(local) * st.step;
     w = (which == 1 ? p.w1 : p.w2) + row0 * st.row_bytes;
     if (kFmt == MOE_W_MXFP4) s = (which == 1 ? p.s1 : p.s2) + row0 * st.srow_bytes;
@@ -307,9 +325,6 @@ struct Loader {
 
   __device__ __forceinline__ void start(const FewParams& p, const FewShared& sh, const Stream& st, int which,
                                         int lane) {
-    g = st.g0;
-    ai = g / st.per_expert;
-    local = g % st.per_expert;
     chunk = 0;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
@@ -323,14 +338,19 @@ struct Loader {
       const int wr = r < 8 ? r : st.up + r - 8;
       soff[i] = ((static_cast<uint32_t>(wr) * st.srow_bytes + st.u0) & ~3u) + 4 * c;
     }
-    if (g < st.g1) granule(p, sh, st, which);
+    if (st.g0 < st.g1) {
+      ai = st.g0 / st.per_expert;
+      seek(p, sh, st, which, st.g0 % st.per_expert);
+    } else {
+      ai = -1;
+    }
   }
 
   // Copy this warp's part of the next stage into its ring slot.
   __device__ __forceinline__ void load(const FewParams& p, const FewShared& sh, const Stream& st, int which,
                                        uint32_t slot, int lane) {
-    const int u = chunk * st.chunk;  // from the warp's first unit
-    const int n = min(st.chunk, st.u1 - st.u0 - u);
+    const int u = chunk * Fmt<kFmt>::kUnits;  // from the warp's first unit
+    const int n = min(Fmt<kFmt>::kUnits, st.u1 - st.u0 - u);
     const int valid = n * (Fmt<kFmt>::kUnitBytes / 16);
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
@@ -353,14 +373,13 @@ struct Loader {
     }
     if (++chunk == st.nchunks) {
       chunk = 0;
-      ++g;
-      if (++local == st.per_expert) {
-        local = 0;
-        ++ai;
-        if (g < st.g1) granule(p, sh, st, which);
+      local += st.sides;
+      if (local < end) {
+        w += st.sides * st.step * st.row_bytes;
+        if (kFmt == MOE_W_MXFP4) s += st.sides * st.step * st.srow_bytes;
       } else {
-        w += st.step * st.row_bytes;
-        if (kFmt == MOE_W_MXFP4) s += st.step * st.srow_bytes;
+        ++ai;
+        seek(p, sh, st, which, 0);
       }
     }
   }
@@ -485,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxBufs; ++i) {
       sm100::mbar_init(sm100::smem_u32(&sh.full[i]), kWarps);
-      sm100::mbar_init(sm100::smem_u32(&sh.empty[i]), 4 * kN);
+      sm100::mbar_init(sm100::smem_u32(&sh.empty[i]), kWarps);
     }
     sm100::fence_mbar_init();
   }
@@ -610,12 +629,11 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
   ld.start(p, sh, st1, 1, lane);
   int ld_which = 1, ld_slot = 0;
   auto issue = [&]() {
-    if (ld_which == 1 && ld.g >= st1.g1) {
+    if (ld_which == 1 && ld.ai < 0) {
       ld_which = 2;
       ld.start(p, sh, st2, 2, lane);
     }
-    const Stream& st = ld_which == 1 ? st1 : st2;
-    if (ld.g < st.g1) ld.load(p, sh, st, ld_which, ring_at + ld_slot * slot_bytes<kFmt>(), lane);
+    if (ld.ai >= 0) ld.load(p, sh, ld_which == 1 ? st1 : st2, ld_which, ring_at + ld_slot * slot_bytes<kFmt>(), lane);
     cp_commit();
     if (++ld_slot == p.stages) ld_slot = 0;
   };
@@ -631,108 +649,143 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
   for (int which = 1; which <= 2; ++which) {
     const Stream& s = which == 1 ? st1 : st2;
     if (which == 2) grid_barrier(p.header, kBar2);  // h is complete
-    int ai = s.g0 / s.per_expert, local = s.g0 % s.per_expert;
-    bool fresh = true;
     // where the lane's two rows' scale bytes start in a slot
     const uint32_t s_lo = 16 * Fmt<kFmt>::kPitch + fr * Fmt<kFmt>::kScalePitch +
                           ((static_cast<uint32_t>(fr) * s.srow_bytes + s.u0) & 3u);
     const uint32_t s_hi = 16 * Fmt<kFmt>::kPitch + (fr + 8) * Fmt<kFmt>::kScalePitch +
                           ((static_cast<uint32_t>(s.up + fr) * s.srow_bytes + s.u0) & 3u);
-    int e = 0, rows = 0, start = 0;
-    uint32_t brow[kN];
-    for (int g = s.g0; g < s.g1; ++g, ++it) {
-      if (fresh) {
-        fresh = false;
-        e = sh.expert[ai];
-        start = sh.start[ai];
-        rows = sh.start[ai + 1] - start;
-        if (which == 2) {
-          __syncthreads();  // the previous expert's rows are read no more
-          if (threadIdx.x < kMaxT) sh.row_max[threadIdx.x] = 0;
-          __syncthreads();
-          load_rows<kFmt>(p, sh, p.h + static_cast<int64_t>(start) * p.I, rows, p.I, act);
-          __syncthreads();
-        }
-        // a column without a token repeats the last row; its sums are not used
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const int n = min(8 * i + fr, rows - 1);
-          brow[i] = act_at + (which == 1 ? nth_bit(sh.tokens[e], n) : n) * p.row_pitch + s.u0 * 64 + fq * 16;
-        }
+    const int split = kWarps / s.sides, tasks = s.sides * 4 * kN;
+    for (int ai = s.g0 / s.per_expert; s.g0 < s.g1 && ai * s.per_expert < s.g1; ++ai) {
+      const int begin = max(0, s.g0 - ai * s.per_expert), end = min(s.per_expert, s.g1 - ai * s.per_expert);
+      const int e = sh.expert[ai], start = sh.start[ai], rows = sh.start[ai + 1] - start;
+      if (which == 2) {
+        __syncthreads();  // the previous expert's rows are read no more
+        if (threadIdx.x < kMaxT) sh.row_max[threadIdx.x] = 0;
+        __syncthreads();
+        load_rows<kFmt>(p, sh, p.h + static_cast<int64_t>(start) * p.I, rows, p.I, act);
+        __syncthreads();
       }
-      // the 4 kN warps that finish this granule (they take turns), and what
-      // they need from memory, asked for before the multiplication
-      const int ew = (warp - it * 4 * kN) & (kWarps - 1);
-      const int grp = ew / 4, at = (ew % 4) * 32 + lane;
-      // fragment element -> weight row r and token n
-      const int r = at / 16 + (at & 2 ? 8 : 0), n = 8 * grp + (at / 4 % 4) * 2 + (at & 1);
-      const bool on = ew < 4 * kN && n < rows;
-      uint16_t bias = 0;
-      if (on)
-        bias = which == 1 ? p.b1[static_cast<int64_t>(e) * 2 * p.I + local * 8 + (r < 8 ? r : p.I + r - 8)]
-                          : p.b2[static_cast<int64_t>(e) * p.D + local * 16 + r];
-      float acc[kN][4];
+      // a column without a token repeats the last row; its sums are not used
+      uint32_t brow[kN];
 #pragma unroll
-      for (int i = 0; i < kN; ++i)
+      for (int i = 0; i < kN; ++i) {
+        const int n = min(8 * i + fr, rows - 1);
+        brow[i] = act_at + (which == 1 ? nth_bit(sh.tokens[e], n) : n) * p.row_pitch + s.u0 * 64 + fq * 16;
+      }
+      // Finish the granules that began at `first`, in turn `turn`: 4 kN tasks
+      // of 128 sums each, spread over the warps.
+      constexpr int kTasks = kN;  // at most, of a warp
+      uint16_t bias[kTasks];
+      auto task_of = [&](int i, int turn) { return ((warp - turn * tasks) & (kWarps - 1)) + kWarps * i; };
+      // What the finish needs from memory, asked for a turn ahead.
+      auto load_bias = [&](int first, int turn) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[i][c] = 0.0f;
-      for (int chunk = 0; chunk < s.nchunks; ++chunk) {
-        cp_wait_upto(p.stages - 1);
-        __syncwarp();
-        const uint32_t at_slot = ring_at + slot * slot_bytes<kFmt>();
-        const int u = chunk * s.chunk, n = min(s.chunk, s.u1 - s.u0 - u);
-        uint32_t b[kN];
+        for (int i = 0; i < kTasks; ++i) {
+          const int task = task_of(i, turn), local = first + task / (4 * kN), at = (task % 4) * 32 + lane;
+          const int r = at / 16 + (at & 2 ? 8 : 0);
+          bias[i] = 0;
+          if (task < tasks && local < end)
+            bias[i] = which == 1 ? p.b1[static_cast<int64_t>(e) * 2 * p.I + local * 8 + (r < 8 ? r : p.I + r - 8)]
+                                 : p.b2[static_cast<int64_t>(e) * p.D + local * 16 + r];
+        }
+      };
+      auto finish = [&](int first, int turn) {
+        const int buf = turn & (p.red_bufs - 1);
+        const uint32_t part = red_at + buf * (kRedFloats * 4);
+        wait_local(full_at + 8 * buf, (turn >> buf_shift) & 1, p.header);
+        float sum[kTasks];
 #pragma unroll
-        for (int i = 0; i < kN; ++i) b[i] = brow[i] + u * 64;
-        if (n == Fmt<kFmt>::kUnits) {
-          mul_units<kFmt, kN, Fmt<kFmt>::kUnits>(at_slot, fr, fq, 0, b, at_slot + s_lo, at_slot + s_hi, acc);
-        } else {
-          for (int j = 0; j < n; ++j) {
-            mul_units<kFmt, kN, 1>(at_slot, fr, fq, j, b, at_slot + s_lo + j, at_slot + s_hi + j, acc);
-#pragma unroll
-            for (int i = 0; i < kN; ++i) b[i] += 64;
+        for (int i = 0; i < kTasks; ++i) {
+          const int task = task_of(i, turn);
+          sum[i] = 0.0f;
+          if (task < tasks) {
+            const int m = task / (4 * kN), grp = task / 4 % kN, at = (task % 4) * 32 + lane;
+#pragma unroll 4
+            for (int w = 0; w < split; ++w)
+              sum[i] += __uint_as_float(lds32(part + (((m * split + w) * kN + grp) * 128 + at) * 4));
           }
         }
         __syncwarp();
-        issue();
-        if (++slot == p.stages) slot = 0;
-      }
-      // the 16 warps' parts meet in buffer it mod red_bufs
-      const int buf = it & (p.red_bufs - 1), round = it >> buf_shift;
-      const uint32_t part = red_at + buf * (kRedFloats * 4);
-      if (round > 0) wait_local(empty_at + 8 * buf, (round - 1) & 1, p.header);
-#pragma unroll
-      for (int i = 0; i < kN; ++i)
-        sm100::st_shared_v4(part + ((warp * kN + i) * 128 + lane * 4) * 4, __float_as_uint(acc[i][0]),
-                            __float_as_uint(acc[i][1]), __float_as_uint(acc[i][2]), __float_as_uint(acc[i][3]));
-      __syncwarp();
-      if (lane == 0) sm100::mbar_arrive(full_at + 8 * buf);
-      if (ew < 4 * kN) {
-        wait_local(full_at + 8 * buf, round & 1, p.header);
-        float v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-          v += __uint_as_float(lds32(part + ((w * kN + grp) * 128 + at) * 4));
-        __syncwarp();
         if (lane == 0) sm100::mbar_arrive(empty_at + 8 * buf);
-        const int row = start + n;
-        if (kFmt == MOE_W_MXFP4 && on)
-          v *= sh.row_scale[which == 1 ? sh.slot[row] / static_cast<uint32_t>(p.k) : n];
-        v += bf16_bits_to_float(bias);
-        if (which == 1) {
-          const float up = __shfl_xor_sync(0xffffffffu, v, 2);
-          if (on && r < 8)
-            p.h[static_cast<int64_t>(row) * p.I + local * 8 + r] = float_to_bf16_bits(glu_act(v, up, p.act));
-        } else if (on) {
+#pragma unroll
+        for (int i = 0; i < kTasks; ++i) {
+          const int task = task_of(i, turn), local = first + task / (4 * kN);
+          if (task >= tasks || local >= end) continue;  // (uniform in a warp)
+          const int grp = task / 4 % kN, at = (task % 4) * 32 + lane;
+          // fragment element -> weight row r and token n
+          const int r = at / 16 + (at & 2 ? 8 : 0), n = 8 * grp + (at / 4 % 4) * 2 + (at & 1);
+          const bool on = n < rows;
+          const int row = start + (on ? n : 0);
           const uint32_t a = sh.slot[row];
-          p.o[static_cast<int64_t>(a) * p.D + local * 16 + r] = sh.gate[a / p.k][a % p.k] * v;
+          float v = sum[i];
+          if (kFmt == MOE_W_MXFP4) v *= sh.row_scale[which == 1 ? a / p.k : on ? n : 0];
+          v += bf16_bits_to_float(bias[i]);
+          if (which == 1) {
+            const float up = __shfl_xor_sync(0xffffffffu, v, 2);
+            if (on && r < 8)
+              p.h[static_cast<int64_t>(row) * p.I + local * 8 + r] = float_to_bf16_bits(glu_act(v, up, p.act));
+          } else if (on) {
+            p.o[static_cast<int64_t>(a) * p.D + local * 16 + r] = sh.gate[a / p.k][a % p.k] * v;
+          }
+        }
+      };
+      for (int base = begin; base < end; base += s.sides, ++it) {
+        float acc[kN][4];
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[i][c] = 0.0f;
+        if (base + s.side < end) {
+          for (int chunk = 0; chunk < s.nchunks; ++chunk) {
+            cp_wait_upto(p.stages - 1);
+            __syncwarp();
+            const uint32_t at_slot = ring_at + slot * slot_bytes<kFmt>();
+            const int u = chunk * Fmt<kFmt>::kUnits, n = min(Fmt<kFmt>::kUnits, s.u1 - s.u0 - u);
+            uint32_t b[kN];
+#pragma unroll
+            for (int i = 0; i < kN; ++i) b[i] = brow[i] + u * 64;
+            if (n == Fmt<kFmt>::kUnits) {
+              mul_units<kFmt, kN, Fmt<kFmt>::kUnits>(at_slot, fr, fq, 0, b, at_slot + s_lo, at_slot + s_hi, acc);
+            } else {
+              int j = 0;
+              if (kFmt == MOE_W_MXFP4 && n >= 4) {
+                mul_units<kFmt, kN, 4>(at_slot, fr, fq, 0, b, at_slot + s_lo, at_slot + s_hi, acc);
+                j = 4;
+#pragma unroll
+                for (int i = 0; i < kN; ++i) b[i] += 256;
+              }
+              for (; j < n; ++j) {
+                mul_units<kFmt, kN, 1>(at_slot, fr, fq, j, b, at_slot + s_lo + j, at_slot + s_hi + j, acc);
+#pragma unroll
+                for (int i = 0; i < kN; ++i) b[i] += 64;
+              }
+            }
+            __syncwarp();
+            issue();
+            if (++slot == p.stages) slot = 0;
+          }
+        }
+        // the warps' parts meet in buffer it mod red_bufs
+        const int buf = it & (p.red_bufs - 1);
+        const uint32_t part = red_at + buf * (kRedFloats * 4);
+        if (it >= p.red_bufs) wait_local(empty_at + 8 * buf, ((it >> buf_shift) - 1) & 1, p.header);
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          sm100::st_shared_v4(part + ((warp * kN + i) * 128 + lane * 4) * 4, __float_as_uint(acc[i][0]),
+                              __float_as_uint(acc[i][1]), __float_as_uint(acc[i][2]), __float_as_uint(acc[i][3]));
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(full_at + 8 * buf);
+        // the previous granules are finished only now, when their parts are
+        // all there; with one buffer these ones are, at once
+        if (p.red_bufs == 1) {
+          load_bias(base, it);
+          finish(base, it);
+        } else {
+          if (base > begin) finish(base - s.sides, it - 1);
+          load_bias(base, it);
         }
       }
-      if (++local == s.per_expert) {
-        local = 0;
-        ++ai;
-        fresh = true;
-      }
+      if (p.red_bufs > 1) finish(begin + (end - begin - 1) / s.sides * s.sides, it - 1);
     }
   }
   cp_wait<0>();

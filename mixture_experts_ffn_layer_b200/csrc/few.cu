@@ -19,10 +19,9 @@
 // A granule is 16 weight rows by the whole reduction. The block's 16 warps
 // split the reduction, so that every SM has work for as little as one token
 // and each warp meets the same slice of the activations in every granule.
-// Each warp streams its slices through its own cp.async ring (no block-wide
-// synchronisation to load; the ring keeps running across granules, experts
-// and from mlp1 into mlp2, whose first weights arrive while the grid barrier
-// is waited for) and multiplies them with mma.sync m16n8k16: the 16 weight
+// The rings run on across granules, experts and from mlp1 into mlp2, whose
+// first weights arrive while the grid barrier is waited for. The multiplication
+// is mma.sync m16n8k16: the 16 weight
 // rows are M, up to 8 tokens are N (two N halves for more than 8). That is
 // the shape this work has -- a 128-row tensor tile would leave the SMs unevenly
 // loaded -- and the tensor rate is far from being a limit. The k index of an
@@ -32,8 +31,15 @@
 // behind mbarriers (full / empty per buffer): a few warps, taking turns, add
 // them in warp order and finish the granule while the others go on.
 //
-// MXFP4: a unit of 32 codes is one scale block. The codes become f16 (exact),
-// the activations f16 with one power of two per row such that the largest
+// bf16: each warp streams its own slices through its own cp.async ring, with
+// no synchronisation between the warps to load.
+//
+// MXFP4: the granules are a quarter of the size and the work on a byte four
+// times as much, so what counts is instructions: a 17th warp brings whole
+// granules in by bulk copies (no instruction of the 16 is spent on loads), and
+// where a block has enough of them the warps work on up to four granules at a
+// time, 16 / that many on each, which leaves fewer partial sums to add. A unit
+// of 32 codes is one scale block. The codes become f16 (exact), the activations f16 with one power of two per row such that the largest
 // magnitude is in [2^8, 2^9) (exact down to 2^-25 of it, absolute error below
 // 2^-33 of it), and each unit's fp32 sum is added with its weight scale.
 //
@@ -64,26 +70,12 @@ constexpr uint64_t kBarrierNs = 1000000000ull;
 // and blocks that are done.
 constexpr int kBar1 = 16, kBar2 = 24, kExit = 32;
 
-template <int kFmt>
-struct Fmt;
-template <>
-struct Fmt<MOE_W_BF16> {
-  static constexpr int kUnitBytes = 64;           // 32 bf16
-  static constexpr int kUnits = 2;                // units per warp and stage: 128 bytes of a row
-  static constexpr int kPitch = 128;              // 16-byte chunks swizzled by row parity
-  static constexpr int kScalePitch = 0;
-};
-template <>
-struct Fmt<MOE_W_MXFP4> {
-  static constexpr int kUnitBytes = 16;           // 32 codes
-  static constexpr int kUnits = 8;                // (a multiple of 4 scale bytes)
-  static constexpr int kPitch = 144;              // odd multiple of 16: 8 rows on distinct banks
-  static constexpr int kScalePitch = 12;          // aligned words covering kUnits scale bytes
-};
-template <int kFmt>
-constexpr int slot_bytes() {
-  return 16 * (Fmt<kFmt>::kPitch + Fmt<kFmt>::kScalePitch);
-}
+// bf16 rings: a stage is 2 units of 32 of 16 rows, 128 bytes of a row, with
+// the 16-byte pieces swizzled by row parity.
+constexpr int kBfUnits = 2, kBfPitch = 128, kBfSlot = 16 * kBfPitch;
+// MXFP4 ring: a stage is a granule, or the part of it over at most
+// kMxChunkUnits units of the reduction.
+constexpr int kMxChunkUnits = 128;
 
 struct FewParams {
   int T, D, E, k, I;
@@ -95,7 +87,8 @@ struct FewParams {
   unsigned* done;    // (D/16) expert granules finished
   uint16_t* y;
   unsigned* header;  // workspace header
-  int stages;
+  int stages;        // of a warp's bf16 ring, or of the block's MXFP4 ring
+  int slab_bytes;    // MXFP4: a stage
   int red_bufs;      // buffers for the warps' partial sums: 4, or 2 or 1 where shared memory is short
   int row_pitch;     // bytes between resident activation rows
   Act act;
@@ -103,9 +96,6 @@ struct FewParams {
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -126,25 +116,16 @@ __device__ __forceinline__ void cp_wait_upto(int n) {
   }
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
+// Shared memory is read through ordinary pointers and the MMAs are not volatile,
+// so that the loads of later units can be scheduled above the MMAs of earlier ones.
+template <class T>
+__device__ __forceinline__ T lds(const uint8_t* at) {
+  return *reinterpret_cast<const T*>(at);
 }
 
 __device__ __forceinline__ void mma_bf16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                                uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -152,14 +133,14 @@ __device__ __forceinline__ void mma_bf16_16816(float (&c)[4], uint32_t a0, uint3
 // The same with f16 operands, and with a zero in place of C.
 __device__ __forceinline__ void mma_f16_16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                                    uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -180,11 +161,14 @@ __device__ __forceinline__ void e2m1_to_f16(uint32_t codes, uint32_t (&p)[4]) {
 // E8M0: 2^(s - 127); the smallest, 2^-127, counts as zero.
 __device__ __forceinline__ float e8m0(uint32_t s) { return __uint_as_float(s << 23); }
 
+// The 16 computing warps meet (an MXFP4 block has a 17th, which loads).
+__device__ __forceinline__ void warps_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+
 // All blocks of the grid meet (the launch is cooperative, so all are
 // resident). Waits at most kBarrierNs, then records the timeout and goes on:
 // every index computed later is in range whatever the data hold.
 __device__ __forceinline__ void grid_barrier(unsigned* header, int which) {
-  __syncthreads();
+  warps_sync();
   if (threadIdx.x == 0) {
     unsigned* count = header + which;
     asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(count) : "memory");
@@ -203,7 +187,7 @@ __device__ __forceinline__ void grid_barrier(unsigned* header, int which) {
       }
     }
   }
-  __syncthreads();
+  warps_sync();
 }
 
 // The last block to leave sets the counters back to zero for the next call
@@ -234,7 +218,8 @@ __device__ __forceinline__ float key_value(uint32_t key) {
 }
 
 struct FewShared {
-  uint64_t full[kMaxBufs], empty[kMaxBufs];  // of the partial-sum buffers
+  uint64_t full[kMaxBufs], empty[kMaxBufs];        // of the partial-sum buffers
+  uint64_t w_full[kMaxStages], w_empty[kMaxStages];  // of the MXFP4 ring
   int n_active;
   uint32_t tokens[256];          // per expert: its tokens, a bit each
   uint8_t place[256];            // per expert: its place among the active ones
@@ -252,7 +237,7 @@ struct FewShared {
 // How many granules a block works on at a time, 16 / that many warps on each:
 // the more, the fewer partial sums meet and the longer each warp's slice; but
 // a block with few granules, or a short reduction, has too little for it.
-__device__ __forceinline__ int pick_sides(int granules, int units) {
+__device__ __forceinline__ int pick_sides(int granules) {
   int sides = 1;
   while (sides < 4 && granules >= 4 * sides) sides *= 2;
   return sides;
@@ -261,15 +246,16 @@ __device__ __forceinline__ int pick_sides(int granules, int units) {
 // One weight's granules as this block and warp see them.
 struct Stream {
   int64_t row_bytes;     // of the weight
-  int srow_bytes;        // of its scales (even; a granule's first row is a multiple of 8 rows into the tensor, so
-                         // a row's scale bytes lie at the same offset from a 4-byte boundary in every granule)
+  int srow_bytes;        // of its scales
   int rows;              // weight rows per expert
   int up;                // row of the 9th weight row relative to the 1st (I: the up half; 8)
   int step;              // weight rows a granule advances by (8 or 16)
   int per_expert;        // granules per expert
   int side, sides;       // this warp's granule of the `sides` that the block works on at a time
   int u0, u1;            // this warp's units of 32 of the reduction
+  int units;             // units of the reduction
   int nchunks;           // stages per granule
+  int chunk;             // MXFP4: units per stage
   int g0, g1;            // this block's granules, over the active experts
 };
 
@@ -277,7 +263,8 @@ template <int kFmt>
 __device__ __forceinline__ Stream make_stream(const FewParams& p, int which, int n_active, int warp) {
   Stream s;
   const int K = which == 1 ? p.D : p.I;
-  s.row_bytes = static_cast<int64_t>(K / 32) * Fmt<kFmt>::kUnitBytes;
+  s.units = K / 32;
+  s.row_bytes = kFmt == MOE_W_BF16 ? 2 * K : K / 2;
   s.srow_bytes = K / 32;
   s.rows = which == 1 ? 2 * p.I : p.D;
   s.up = which == 1 ? p.I : 8;
@@ -286,97 +273,67 @@ __device__ __forceinline__ Stream make_stream(const FewParams& p, int which, int
   const uint32_t n = n_active * s.per_expert;  // at most 128 * 2048
   s.g0 = static_cast<int>(n * blockIdx.x / gridDim.x);
   s.g1 = static_cast<int>(n * (blockIdx.x + 1) / gridDim.x);
-  s.sides = pick_sides(n / gridDim.x, K / 32);
+  s.sides = kFmt == MOE_W_MXFP4 ? pick_sides(n / gridDim.x) : 1;
   const int split = kWarps / s.sides;
   s.side = warp / split;
-  const int units = K / 32, per = (units + split - 1) / split;
-  s.nchunks = (per + Fmt<kFmt>::kUnits - 1) / Fmt<kFmt>::kUnits;
-  s.u0 = min(units, warp % split * per);
-  s.u1 = min(units, s.u0 + per);
+  // bf16: this warp's units, two a stage; MXFP4: stages of nearly equal parts
+  const int per = (s.units + split - 1) / split;
+  s.u0 = min(s.units, warp % split * per);
+  s.u1 = min(s.units, s.u0 + per);
+  s.nchunks = kFmt == MOE_W_BF16 ? (per + kBfUnits - 1) / kBfUnits : (s.units + kMxChunkUnits - 1) / kMxChunkUnits;
+  s.chunk = (s.units + s.nchunks - 1) / s.nchunks;
   return s;
 }
 
-template <int kFmt>
+// The loading end of a warp's bf16 ring: where its next stage comes from, and
+// which 16-byte pieces each lane copies.
 struct Loader {
-  static constexpr int kRowChunks = Fmt<kFmt>::kUnits * Fmt<kFmt>::kUnitBytes / 16;  // 16-byte pieces of a row
-  static constexpr int kPieces = 16 * kRowChunks / 32;
-  static constexpr int kWords = kFmt == MOE_W_MXFP4 ? 2 : 0;
-  uint32_t off[kPieces];        // from the granule's first row, this warp's first unit
-  uint32_t soff[kWords + 1];
-  const uint8_t *w, *s;         // the current granule's first row
+  uint32_t off[4];              // from the granule's first row, this warp's first unit
+  const uint8_t* w;             // the current granule's first row
   int ai, local, end, chunk;    // active expert (-1: no more), granule, end of the expert's granules, stage
 
-  // To the warp's first granule from `ai` on, whose granules begin at `begin`.
+  // To the first granule `begin` of active expert ai.
   __device__ __forceinline__ void seek(const FewParams& p, const FewShared& sh, const Stream& st, int which,
                                        int begin) {
-    for (;; ++ai, begin = 0) {
-      if (ai * st.per_expert >= st.g1) {
-        ai = -1;
-        return;
-      }
-      end = min(st.per_expert, st.g1 - ai * st.per_expert);
-      local = begin + st.side;
-      if (local < end) break;
+    if (ai * st.per_expert >= st.g1) {
+      ai = -1;
+      return;
     }
-    const int64_t row0 = static_cast<int64_t>(sh.expert[ai]) * st.rows + static_cast<int64_t>(local) * st.step;
-    w = (which == 1 ? p.w1 : p.w2) + row0 * st.row_bytes;
-    if (kFmt == MOE_W_MXFP4) s = (which == 1 ? p.s1 : p.s2) + row0 * st.srow_bytes;
+    end = min(st.per_expert, st.g1 - ai * st.per_expert);
+    local = begin;
+    w = (which == 1 ? p.w1 : p.w2) +
+        (static_cast<int64_t>(sh.expert[ai]) * st.rows + static_cast<int64_t>(local) * st.step) * st.row_bytes;
   }
 
   __device__ __forceinline__ void start(const FewParams& p, const FewShared& sh, const Stream& st, int which,
                                         int lane) {
     chunk = 0;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int idx = lane + 32 * i, r = idx / kRowChunks, c = idx % kRowChunks;
-      const int wr = r < 8 ? r : st.up + r - 8;
-      off[i] = static_cast<uint32_t>(wr * st.row_bytes + st.u0 * Fmt<kFmt>::kUnitBytes + c * 16);
+    for (int i = 0; i < 4; ++i) {
+      const int idx = lane + 32 * i, r = idx / 8, c = idx % 8;
+      off[i] = static_cast<uint32_t>((r < 8 ? r : st.up + r - 8) * st.row_bytes + st.u0 * 64 + c * 16);
     }
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      const int idx = lane + 32 * i, r = idx / 3, c = idx % 3;
-      const int wr = r < 8 ? r : st.up + r - 8;
-      soff[i] = ((static_cast<uint32_t>(wr) * st.srow_bytes + st.u0) & ~3u) + 4 * c;
-    }
+    ai = -1;
     if (st.g0 < st.g1) {
       ai = st.g0 / st.per_expert;
       seek(p, sh, st, which, st.g0 % st.per_expert);
-    } else {
-      ai = -1;
     }
   }
 
   // Copy this warp's part of the next stage into its ring slot.
   __device__ __forceinline__ void load(const FewParams& p, const FewShared& sh, const Stream& st, int which,
                                        uint32_t slot, int lane) {
-    const int u = chunk * Fmt<kFmt>::kUnits;  // from the warp's first unit
-    const int n = min(Fmt<kFmt>::kUnits, st.u1 - st.u0 - u);
-    const int valid = n * (Fmt<kFmt>::kUnitBytes / 16);
+    const int u = chunk * kBfUnits;  // from the warp's first unit
+    const int valid = min(kBfUnits, st.u1 - st.u0 - u) * 4;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int idx = lane + 32 * i, r = idx / kRowChunks, c = idx % kRowChunks;
-      const int cc = kFmt == MOE_W_BF16 ? c ^ ((r & 1) << 2) : c;
-      if (c < valid)
-        cp_async16(slot + r * Fmt<kFmt>::kPitch + cc * 16, w + off[i] + u * Fmt<kFmt>::kUnitBytes);
-    }
-    if (kFmt == MOE_W_MXFP4) {
-      // the aligned words that hold the scale bytes of units [u, u + n): u is
-      // a multiple of 4 (the tensor's size too, so the words lie inside it)
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) {
-        const int idx = lane + 32 * i, r = idx / 3, c = idx % 3;
-        const int wr = r < 8 ? r : st.up + r - 8;
-        const int lead = static_cast<int>((static_cast<uint32_t>(wr) * st.srow_bytes + st.u0) & 3u);
-        if (r < 16 && n > 0 && 4 * c < lead + n)
-          cp_async4(slot + 16 * Fmt<kFmt>::kPitch + r * Fmt<kFmt>::kScalePitch + 4 * c, s + soff[i] + u);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int idx = lane + 32 * i, r = idx / 8, c = idx % 8;
+      if (c < valid) cp_async16(slot + r * kBfPitch + (c ^ ((r & 1) << 2)) * 16, w + off[i] + u * 64);
     }
     if (++chunk == st.nchunks) {
       chunk = 0;
-      local += st.sides;
-      if (local < end) {
-        w += st.sides * st.step * st.row_bytes;
-        if (kFmt == MOE_W_MXFP4) s += st.sides * st.step * st.srow_bytes;
+      if (++local < end) {
+        w += st.step * st.row_bytes;
       } else {
         ++ai;
         seek(p, sh, st, which, 0);
@@ -385,49 +342,128 @@ struct Loader {
   }
 };
 
-// Multiply kUnits landed units: acc (kN groups of 8 tokens) += 16 weight rows
-// x the units. `a`: the lane's place in its row of the slot; `b`: in its rows
-// of the activations; `s_lo`, `s_hi`: of its rows' scales.
-template <int kFmt, int kN, int kUnits>
-__device__ __forceinline__ void mul_units(uint32_t slot, int r, int q, int j0, const uint32_t (&b)[kN], uint32_t s_lo,
-                                          uint32_t s_hi, float (&acc)[kN][4]) {
+// Bytes between a stage's rows of codes. Rows 32 or 96 bytes off a multiple of
+// 128 collide two ways at most and are copied as they lie, 8 at a time; others
+// are copied row by row to an odd multiple of 16 (no collision).
+__host__ __device__ constexpr bool mx_as_stored(int units, int nchunks) { return nchunks == 1 && units % 4 == 2; }
+__host__ __device__ constexpr int mx_pitch(int units, int nchunks, int chunk) {
+  return mx_as_stored(units, nchunks) ? units * 16 : (chunk | 1) * 16;
+}
+
+// The loading warp of an MXFP4 block: every granule of the block in order,
+// mlp1's then mlp2's.
+__device__ __forceinline__ void mx_produce(const FewParams& p, FewShared& sh, const Stream& st1, const Stream& st2,
+                                           uint32_t ring, int lane) {
+  using namespace sm100;
+  const uint32_t full = smem_u32(sh.w_full), empty = smem_u32(sh.w_empty);
+  int slot = 0, issued = 0;
+  uint32_t phase = 0;
+  bool failed = false;
+  for (int which = 1; which <= 2 && !failed; ++which) {
+    const Stream& st = which == 1 ? st1 : st2;
+    const int pitch = mx_pitch(st.units, st.nchunks, st.chunk);
+    const bool as_stored = mx_as_stored(st.units, st.nchunks);
+    for (int g = st.g0; g < st.g1 && !failed; ++g) {
+      const int ai = g / st.per_expert, local = g % st.per_expert;
+      const int64_t row0 = static_cast<int64_t>(sh.expert[ai]) * st.rows + static_cast<int64_t>(local) * st.step;
+      const uint8_t* w = (which == 1 ? p.w1 : p.w2) + row0 * st.row_bytes;
+      const uint8_t* s = (which == 1 ? p.s1 : p.s2) + row0 * st.srow_bytes;
+      for (int c = 0; c < st.nchunks; ++c) {
+        if (!mbar_wait_bounded(empty + 8 * slot, phase ^ 1u, nullptr, kBarrierNs)) {
+          failed = true;
+          break;
+        }
+        const int n = min(st.chunk, st.units - c * st.chunk);
+        const uint32_t bar = full + 8 * slot, to = ring + slot * p.slab_bytes;
+        if (lane == 0) mbar_arrive_expect_tx(bar, 16 * (n * 16 + st.srow_bytes));
+        __syncwarp();
+        if (as_stored) {
+          if (lane < 2) bulk_load(to + lane * 8 * pitch, w + lane * st.up * st.row_bytes, 8 * pitch, bar);
+        } else if (lane < 16) {
+          const int wr = lane < 8 ? lane : st.up + lane - 8;
+          bulk_load(to + lane * pitch, w + wr * st.row_bytes + c * st.chunk * 16, n * 16, bar);
+        }
+        // all of the 16 rows' scales, with every stage of the granule
+        if (lane == 16 || lane == 17)
+          bulk_load(to + 16 * pitch + (lane - 16) * 8 * st.srow_bytes,
+                    s + static_cast<int64_t>(lane - 16) * st.up * st.srow_bytes, 8 * st.srow_bytes, bar);
+        ++issued;
+        if (++slot == p.stages) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  }
+  if (failed) {
+    if (lane == 0) record_status(reinterpret_cast<int*>(p.header), MOE_ERR_TIMEOUT);
+    // the copies still in flight land before the block can exit
+    for (int i = min(issued, p.stages); i > 0; --i) {
+      if (--slot < 0) {
+        slot = p.stages - 1;
+        phase ^= 1u;
+      }
+      mbar_wait_bounded(full + 8 * slot, phase, nullptr, kBarrierNs);
+    }
+  }
+}
+
+// acc (kN groups of 8 tokens) += 16 weight rows x n <= 2 units of a bf16 stage.
+// Two units of a row are 8 pieces of 16 bytes: piece 4 j + q, the halves
+// exchanged in odd rows (conflict-free). `b`: the lane's place in its rows of
+// the activations.
+template <int kN>
+__device__ __forceinline__ void mul_bf16(const uint8_t* slot, int r, int q, int n, const uint8_t* const (&b)[kN],
+                                         float (&acc)[kN][4]) {
 #pragma unroll
-  for (int j = 0; j < kUnits; ++j) {
-    if (kFmt == MOE_W_BF16) {
-      // two units of a row are 8 chunks of 16 bytes: chunk 4*j + q, the halves
-      // exchanged in odd rows (conflict-free)
-      const uint32_t at = slot + r * Fmt<kFmt>::kPitch + (((4 * (j0 + j) + q) ^ ((r & 1) << 2)) * 16);
-      const uint4 a = lds128(at), a8 = lds128(at + 8 * Fmt<kFmt>::kPitch);
+  for (int j = 0; j < kBfUnits; ++j) {
+    if (j < n) {
+      const uint8_t* at = slot + r * kBfPitch + (((4 * j + q) ^ ((r & 1) << 2)) * 16);
+      const uint4 a = lds<uint4>(at), a8 = lds<uint4>(at + 8 * kBfPitch);
 #pragma unroll
       for (int g = 0; g < kN; ++g) {
-        const uint4 v = lds128(b[g] + j * 64);
+        const uint4 v = lds<uint4>(b[g] + j * 64);
         mma_bf16_16816(acc[g], a.x, a8.x, a.y, a8.y, v.x, v.y);
         mma_bf16_16816(acc[g], a.z, a8.z, a.w, a8.w, v.z, v.w);
-      }
-    } else {
-      const uint32_t at = slot + r * Fmt<kFmt>::kPitch + q * 4 + (j0 + j) * 16;
-      uint32_t a[4], a8[4];
-      e2m1_to_f16(lds32(at), a);
-      e2m1_to_f16(lds32(at + 8 * Fmt<kFmt>::kPitch), a8);
-      const float w_lo = e8m0(lds8(s_lo + j)), w_hi = e8m0(lds8(s_hi + j));
-#pragma unroll
-      for (int g = 0; g < kN; ++g) {
-        const uint4 v = lds128(b[g] + j * 64);
-        float c[4];
-        mma_f16_16816_zero(c, a[0], a8[0], a[1], a8[1], v.x, v.y);
-        mma_f16_16816(c, a[2], a8[2], a[3], a8[3], v.z, v.w);
-        acc[g][0] = fmaf(w_lo, c[0], acc[g][0]);
-        acc[g][1] = fmaf(w_lo, c[1], acc[g][1]);
-        acc[g][2] = fmaf(w_hi, c[2], acc[g][2]);
-        acc[g][3] = fmaf(w_hi, c[3], acc[g][3]);
       }
     }
   }
 }
 
+// The same for kUnits units of MXFP4 codes; at, at8: the lane's place in its
+// two rows of codes, s_lo, s_hi: in their scales. All four and b move on.
+template <int kN, int kUnits>
+__device__ __forceinline__ void mul_mx(const uint8_t*& at, const uint8_t*& at8, const uint8_t*& s_lo,
+                                       const uint8_t*& s_hi, const uint8_t* (&b)[kN], float (&acc)[kN][4]) {
+#pragma unroll
+  for (int j = 0; j < kUnits; ++j) {
+    uint32_t a[4], a8[4];
+    e2m1_to_f16(lds<uint32_t>(at + j * 16), a);
+    e2m1_to_f16(lds<uint32_t>(at8 + j * 16), a8);
+    const float w_lo = e8m0(lds<uint8_t>(s_lo + j)), w_hi = e8m0(lds<uint8_t>(s_hi + j));
+#pragma unroll
+    for (int g = 0; g < kN; ++g) {
+      const uint4 v = lds<uint4>(b[g] + j * 64);
+      float c[4];
+      mma_f16_16816_zero(c, a[0], a8[0], a[1], a8[1], v.x, v.y);
+      mma_f16_16816(c, a[2], a8[2], a[3], a8[3], v.z, v.w);
+      acc[g][0] = fmaf(w_lo, c[0], acc[g][0]);
+      acc[g][1] = fmaf(w_lo, c[1], acc[g][1]);
+      acc[g][2] = fmaf(w_hi, c[2], acc[g][2]);
+      acc[g][3] = fmaf(w_hi, c[3], acc[g][3]);
+    }
+  }
+  at += kUnits * 16;
+  at8 += kUnits * 16;
+  s_lo += kUnits;
+  s_hi += kUnits;
+#pragma unroll
+  for (int g = 0; g < kN; ++g) b[g] += kUnits * 64;
+}
+
 // Bring `rows` rows of K bf16 into shared memory; MXFP4 rows become f16
-// scaled by a power of two. row_max is zero on entry, and the block
-// synchronises before it reads the rows.
+// scaled by a power of two. row_max is zero on entry, and the warps
+// synchronise before they read the rows.
 template <int kFmt>
 __device__ __forceinline__ void load_rows(const FewParams& p, FewShared& sh, const uint16_t* from, int rows, int K,
                                           uint8_t* act) {
@@ -456,7 +492,7 @@ __device__ __forceinline__ void load_rows(const FewParams& p, FewShared& sh, con
     }
   }
   if (kFmt == MOE_W_MXFP4) {
-    __syncthreads();
+    warps_sync();
     for (int i = threadIdx.x; i < total; i += kThreads) {
       const int n = i / per, c = i - n * per;
       // 2^shift brings the row's largest magnitude into [2^8, 2^9); a row of
@@ -486,7 +522,7 @@ __device__ __forceinline__ int nth_bit(uint32_t mask, int n) {
 }
 
 template <int kFmt, int kN>
-__global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
+__global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 : 0), 1) few_kernel(const FewParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   // resident rows | partial sums | rings
   uint8_t* act = smem;
@@ -497,6 +533,22 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
 
   // (the shuffle tells the compiler that the warp index is uniform)
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0), lane = threadIdx.x % 32;
+
+  if (kFmt == MOE_W_MXFP4) {
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < p.stages; ++i) {
+        sm100::mbar_init(sm100::smem_u32(&sh.w_full[i]), 1);
+        sm100::mbar_init(sm100::smem_u32(&sh.w_empty[i]), kWarps);
+      }
+      sm100::fence_mbar_init();
+    }
+    if (warp == kWarps) {
+      __syncthreads();  // the lists are complete
+      mx_produce(p, sh, make_stream<kFmt>(p, 1, sh.n_active, 0), make_stream<kFmt>(p, 2, sh.n_active, 0),
+                 sm100::smem_u32(ring), lane);
+      return;
+    }
+  }
 
   // ---- router logits; the tokens' rows; the completion counters start at zero
   if (threadIdx.x < 256) sh.tokens[threadIdx.x] = 0;
@@ -542,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
           sh.dot[warp] = sum;
       }
     }
-    __syncthreads();
+    warps_sync();
     if (parts > 1 && static_cast<int>(threadIdx.x) < n) {  // (then every logit had its own group)
       float sum = 0.0f;
       for (int i = 0; i < parts; ++i) sum += sh.dot[threadIdx.x * parts + i];
@@ -587,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
     }
     if (lane < p.k) sh.gate[warp][lane] = __fdividef(mine, total);
   }
-  __syncthreads();
+  warps_sync();
   if (warp == 0) {
     int n = 0, rows = 0;  // active experts and rows before expert 32 i
     for (int base = 0; base < p.E; base += 32) {
@@ -614,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
       sh.start[n] = static_cast<uint8_t>(rows);
     }
   }
-  __syncthreads();
+  warps_sync();
   if (static_cast<int>(threadIdx.x) < p.T * p.k) {
     const int t = threadIdx.x / p.k, e = sh.top[t][threadIdx.x % p.k];
     sh.slot[sh.start[sh.place[e]] + __popc(sh.tokens[e] & ((1u << t) - 1u))] = static_cast<uint8_t>(threadIdx.x);
@@ -624,53 +676,51 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
   // ---- the weight stream: mlp1's stages, then mlp2's, through this warp's ring
   const Stream st1 = make_stream<kFmt>(p, 1, n_active, warp);
   const Stream st2 = make_stream<kFmt>(p, 2, n_active, warp);
-  const uint32_t ring_at = sm100::smem_u32(ring) + warp * p.stages * slot_bytes<kFmt>();
-  Loader<kFmt> ld;
-  ld.start(p, sh, st1, 1, lane);
+  const uint8_t* ring_mine = ring + warp * p.stages * kBfSlot;  // bf16
+  const uint32_t ring_at = sm100::smem_u32(ring_mine);
+  Loader ld;
+  if (kFmt == MOE_W_BF16) ld.start(p, sh, st1, 1, lane);
   int ld_which = 1, ld_slot = 0;
   auto issue = [&]() {
     if (ld_which == 1 && ld.ai < 0) {
       ld_which = 2;
       ld.start(p, sh, st2, 2, lane);
     }
-    if (ld.ai >= 0) ld.load(p, sh, ld_which == 1 ? st1 : st2, ld_which, ring_at + ld_slot * slot_bytes<kFmt>(), lane);
+    if (ld.ai >= 0) ld.load(p, sh, ld_which == 1 ? st1 : st2, ld_which, ring_at + ld_slot * kBfSlot, lane);
     cp_commit();
     if (++ld_slot == p.stages) ld_slot = 0;
   };
-  for (int i = 0; i < p.stages; ++i) issue();
+  if (kFmt == MOE_W_BF16)
+    for (int i = 0; i < p.stages; ++i) issue();
   __syncthreads();  // the lists are complete
 
-  int slot = 0, it = 0;
+  int slot = 0, it = 0;     // of the ring; turn
+  uint32_t slab_phase = 0;  // MXFP4: of the ring
   const int buf_shift = p.red_bufs >> 1;  // log2 of 1, 2 or 4
-  const uint32_t act_at = sm100::smem_u32(act), red_at = sm100::smem_u32(red);
   const uint32_t full_at = sm100::smem_u32(sh.full), empty_at = sm100::smem_u32(sh.empty);
   const int fr = lane / 4, fq = lane % 4;
 #pragma unroll 1
   for (int which = 1; which <= 2; ++which) {
     const Stream& s = which == 1 ? st1 : st2;
     if (which == 2) grid_barrier(p.header, kBar2);  // h is complete
-    // where the lane's two rows' scale bytes start in a slot
-    const uint32_t s_lo = 16 * Fmt<kFmt>::kPitch + fr * Fmt<kFmt>::kScalePitch +
-                          ((static_cast<uint32_t>(fr) * s.srow_bytes + s.u0) & 3u);
-    const uint32_t s_hi = 16 * Fmt<kFmt>::kPitch + (fr + 8) * Fmt<kFmt>::kScalePitch +
-                          ((static_cast<uint32_t>(s.up + fr) * s.srow_bytes + s.u0) & 3u);
+    const int pitch = mx_pitch(s.units, s.nchunks, s.chunk);
     const int split = kWarps / s.sides, tasks = s.sides * 4 * kN;
     for (int ai = s.g0 / s.per_expert; s.g0 < s.g1 && ai * s.per_expert < s.g1; ++ai) {
       const int begin = max(0, s.g0 - ai * s.per_expert), end = min(s.per_expert, s.g1 - ai * s.per_expert);
       const int e = sh.expert[ai], start = sh.start[ai], rows = sh.start[ai + 1] - start;
       if (which == 2) {
-        __syncthreads();  // the previous expert's rows are read no more
+        warps_sync();  // the previous expert's rows are read no more
         if (threadIdx.x < kMaxT) sh.row_max[threadIdx.x] = 0;
-        __syncthreads();
+        warps_sync();
         load_rows<kFmt>(p, sh, p.h + static_cast<int64_t>(start) * p.I, rows, p.I, act);
-        __syncthreads();
+        warps_sync();
       }
       // a column without a token repeats the last row; its sums are not used
-      uint32_t brow[kN];
+      const uint8_t* brow[kN];
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
         const int n = min(8 * i + fr, rows - 1);
-        brow[i] = act_at + (which == 1 ? nth_bit(sh.tokens[e], n) : n) * p.row_pitch + s.u0 * 64 + fq * 16;
+        brow[i] = act + (which == 1 ? nth_bit(sh.tokens[e], n) : n) * p.row_pitch + (kFmt == MOE_W_BF16 ? s.u0 * 64 : 0) + fq * 16;
       }
       // Finish the granules that began at `first`, in turn `turn`: 4 kN tasks
       // of 128 sums each, spread over the warps.
@@ -691,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
       };
       auto finish = [&](int first, int turn) {
         const int buf = turn & (p.red_bufs - 1);
-        const uint32_t part = red_at + buf * (kRedFloats * 4);
+        const float* part = red + buf * kRedFloats;
         wait_local(full_at + 8 * buf, (turn >> buf_shift) & 1, p.header);
         float sum[kTasks];
 #pragma unroll
@@ -702,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
             const int m = task / (4 * kN), grp = task / 4 % kN, at = (task % 4) * 32 + lane;
 #pragma unroll 4
             for (int w = 0; w < split; ++w)
-              sum[i] += __uint_as_float(lds32(part + (((m * split + w) * kN + grp) * 128 + at) * 4));
+              sum[i] += part[((m * split + w) * kN + grp) * 128 + at];
           }
         }
         __syncwarp();
@@ -735,44 +785,62 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
         for (int i = 0; i < kN; ++i)
 #pragma unroll
           for (int c = 0; c < 4; ++c) acc[i][c] = 0.0f;
-        if (base + s.side < end) {
+        if (kFmt == MOE_W_BF16) {
           for (int chunk = 0; chunk < s.nchunks; ++chunk) {
             cp_wait_upto(p.stages - 1);
             __syncwarp();
-            const uint32_t at_slot = ring_at + slot * slot_bytes<kFmt>();
-            const int u = chunk * Fmt<kFmt>::kUnits, n = min(Fmt<kFmt>::kUnits, s.u1 - s.u0 - u);
-            uint32_t b[kN];
+            const int u = chunk * kBfUnits;
+            const uint8_t* b[kN];
 #pragma unroll
             for (int i = 0; i < kN; ++i) b[i] = brow[i] + u * 64;
-            if (n == Fmt<kFmt>::kUnits) {
-              mul_units<kFmt, kN, Fmt<kFmt>::kUnits>(at_slot, fr, fq, 0, b, at_slot + s_lo, at_slot + s_hi, acc);
-            } else {
-              int j = 0;
-              if (kFmt == MOE_W_MXFP4 && n >= 4) {
-                mul_units<kFmt, kN, 4>(at_slot, fr, fq, 0, b, at_slot + s_lo, at_slot + s_hi, acc);
-                j = 4;
-#pragma unroll
-                for (int i = 0; i < kN; ++i) b[i] += 256;
-              }
-              for (; j < n; ++j) {
-                mul_units<kFmt, kN, 1>(at_slot, fr, fq, j, b, at_slot + s_lo + j, at_slot + s_hi + j, acc);
-#pragma unroll
-                for (int i = 0; i < kN; ++i) b[i] += 64;
-              }
-            }
+            mul_bf16<kN>(ring_mine + slot * kBfSlot, fr, fq, s.u1 - s.u0 - u, b, acc);
             __syncwarp();
             issue();
             if (++slot == p.stages) slot = 0;
           }
+        } else {
+          // Every warp waits for every stage of the turn, in order, and frees
+          // it -- at once where the stage belongs to another side -- so that no
+          // slot's phase passes a warp by.
+          const int mine = s.side * s.nchunks, all = min(s.sides, end - base) * s.nchunks;
+          for (int i = 0; i < all; ++i) {
+            wait_local(sm100::smem_u32(&sh.w_full[slot]), slab_phase, p.header);
+            const int chunk = i - mine;
+            if (chunk >= 0 && chunk < s.nchunks) {
+              // this warp's units of the stage
+              const int first = chunk * s.chunk, n = min(s.chunk, s.units - first), per = (n + split - 1) / split;
+              const int u0 = min(n, warp % split * per);
+              int left = min(n, u0 + per) - u0;
+              const uint8_t* at = ring + slot * p.slab_bytes + fr * pitch + u0 * 16 + fq * 4;
+              const uint8_t* at8 = at + 8 * pitch;
+              const uint8_t* s_lo = ring + slot * p.slab_bytes + 16 * pitch + fr * s.srow_bytes + first + u0;
+              const uint8_t* s_hi = s_lo + 8 * s.srow_bytes;
+              const uint8_t* b[kN];
+#pragma unroll
+              for (int j = 0; j < kN; ++j) b[j] = brow[j] + (first + u0) * 64;
+              for (; left >= 8; left -= 8) mul_mx<kN, 8>(at, at8, s_lo, s_hi, b, acc);
+              if (left >= 4) {
+                mul_mx<kN, 4>(at, at8, s_lo, s_hi, b, acc);
+                left -= 4;
+              }
+              for (; left > 0; --left) mul_mx<kN, 1>(at, at8, s_lo, s_hi, b, acc);
+            }
+            __syncwarp();
+            if (lane == 0) sm100::mbar_arrive(sm100::smem_u32(&sh.w_empty[slot]));
+            if (++slot == p.stages) {
+              slot = 0;
+              slab_phase ^= 1u;
+            }
+          }
         }
         // the warps' parts meet in buffer it mod red_bufs
         const int buf = it & (p.red_bufs - 1);
-        const uint32_t part = red_at + buf * (kRedFloats * 4);
+        float* part = red + buf * kRedFloats;
         if (it >= p.red_bufs) wait_local(empty_at + 8 * buf, ((it >> buf_shift) - 1) & 1, p.header);
 #pragma unroll
         for (int i = 0; i < kN; ++i)
-          sm100::st_shared_v4(part + ((warp * kN + i) * 128 + lane * 4) * 4, __float_as_uint(acc[i][0]),
-                              __float_as_uint(acc[i][1]), __float_as_uint(acc[i][2]), __float_as_uint(acc[i][3]));
+          *reinterpret_cast<float4*>(part + (warp * kN + i) * 128 + lane * 4) =
+              make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
         __syncwarp();
         if (lane == 0) sm100::mbar_arrive(full_at + 8 * buf);
         // the previous granules are finished only now, when their parts are
@@ -791,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
   cp_wait<0>();
 
   // ---- combine: the block whose granule is the last of its 16 columns
-  __syncthreads();
+  warps_sync();
   const int n2 = st2.g1 - st2.g0;
   for (int base = 0; base < n2; base += kMaxActive) {
     const int cnt = min(kMaxActive, n2 - base);
@@ -802,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
       __threadfence();
       sh.last[threadIdx.x] = last ? dg : -1;
     }
-    __syncthreads();
+    warps_sync();
     const int per = p.T * 16;
     for (int i = threadIdx.x; i < cnt * per; i += kThreads) {
       const int dg = sh.last[i / per];
@@ -812,27 +880,36 @@ __global__ void __launch_bounds__(kThreads, 1) few_kernel(const FewParams p) {
       for (int j = 0; j < p.k; ++j) v += __ldcg(p.o + static_cast<int64_t>(t * p.k + j) * p.D + d0);
       p.y[static_cast<int64_t>(t) * p.D + d0] = float_to_bf16_bits(v);
     }
-    __syncthreads();
+    warps_sync();
   }
   grid_exit(p.header);
 }
 
 template <int kFmt, int kN>
 moe_status_t launch(FewParams p, cudaStream_t s) {
-  const int red = kWarps * 128 * kN * 4, slots = kWarps * slot_bytes<kFmt>();
-  const int room = kMaxSmem - 4096 - p.T * p.row_pitch;
+  constexpr bool mx = kFmt == MOE_W_MXFP4;
+  const int red = kWarps * 128 * kN * 4;
+  if (mx) {
+    for (const int K : {p.D, p.I}) {
+      const int units = K / 32, nchunks = (units + kMxChunkUnits - 1) / kMxChunkUnits;
+      const int bytes = 16 * (mx_pitch(units, nchunks, (units + nchunks - 1) / nchunks) + units);
+      if (bytes > p.slab_bytes) p.slab_bytes = (bytes + 127) / 128 * 128;
+    }
+  }
+  const int stage = mx ? p.slab_bytes : kWarps * kBfSlot;
   // the partial sums' buffers after two stages, then as many stages as fit
-  p.red_bufs = kN == 1 && room - 4 * red >= 2 * slots ? 4 : room - 2 * red >= 2 * slots ? 2 : 1;
-  const int fixed = p.T * p.row_pitch + p.red_bufs * red;
-  int stages = (room - p.red_bufs * red) / slots;
+  const int room = kMaxSmem - 4096 - p.T * p.row_pitch;
+  p.red_bufs = kN == 1 && room - 4 * red >= 2 * stage ? 4 : room - 2 * red >= 2 * stage ? 2 : 1;
+  int stages = (room - p.red_bufs * red) / stage;
   if (stages > kMaxStages) stages = kMaxStages;
   if (stages < 2) return MOE_ERR_UNSUPPORTED;
   p.stages = stages;
-  const int smem = fixed + stages * slots;
+  const int smem = p.T * p.row_pitch + p.red_bufs * red + stages * stage;
   if (cudaFuncSetAttribute(few_kernel<kFmt, kN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return MOE_ERR_CUDA;
   void* args[] = {&p};
-  if (cudaLaunchCooperativeKernel(reinterpret_cast<void*>(few_kernel<kFmt, kN>), dim3(num_sms()), dim3(kThreads), args,
+  if (cudaLaunchCooperativeKernel(reinterpret_cast<void*>(few_kernel<kFmt, kN>), dim3(num_sms()),
+                                  dim3(kThreads + (mx ? 32 : 0)), args,
                                   smem, s) != cudaSuccess) {
     cudaGetLastError();
     return MOE_ERR_CUDA;

@@ -14,7 +14,7 @@ namespace {
 
 struct WsLayout {
   size_t block_counts, topk_idx, topk_w, counts, offsets, perm, inv, x_perm, h, o_perm, xq, x_sf, hq, h_sf,
-      mx_prep, route_partial, few_logits, few_done, total;
+      mx_prep, route_partial, few_logits, total;
 };
 
 WsLayout ws_layout(const moe_dims_t& d) {
@@ -47,10 +47,7 @@ WsLayout ws_layout(const moe_dims_t& d) {
     L.h_sf = take(mx_sf_bytes(d, d.I));
     L.mx_prep = take(mx_prep_bytes(d));
   }
-  if (d.T <= few_max_tokens(d)) {  // the one-launch layer: its logits and completion counters
-    L.few_logits = take(static_cast<size_t>(d.T) * d.E * 4);
-    L.few_done = take(static_cast<size_t>(d.D) / 16 * 4);
-  }
+  if (d.T <= few_max_tokens(d)) L.few_logits = take(static_cast<size_t>(d.T) * d.E * 4);  // the one-launch layer
   L.total = off;
   return L;
 }
@@ -282,7 +279,7 @@ moe_status_t moe_forward_few(moe_dims_t d, const uint16_t* x, const uint16_t* Wr
   MOE_TRY(check_ws(d, ws, ws_bytes));
   const WsLayout L = ws_layout(d);
   return launch_few(d, x, Wr, br, W1, b1, W2, b2, y, at<float>(ws, L.few_logits), at<uint16_t>(ws, L.h),
-                    at<float>(ws, L.o_perm), at<unsigned>(ws, L.few_done), ws, static_cast<cudaStream_t>(stream));
+                    at<float>(ws, L.o_perm), ws, static_cast<cudaStream_t>(stream));
 }
 
 moe_status_t moe_rmsnorm(moe_norm_t n, const uint16_t* x, const void* residual, const uint16_t* gamma, void* res_out,

@@ -84,11 +84,11 @@ cudaError_t launch_rmsnorm(const moe_norm_t& n, const uint16_t* x, const void* r
                            void* res_out, uint16_t* y, uint8_t* q, float* q_scale, cudaStream_t s);
 
 // The whole layer for at most few_max_tokens(d) tokens in one launch (few.cu).
-// logits (T, E), h (T*k, I), o (T*k, D) and done (D/16) are scratch.
+// logits (T, E), h (T*k, I) and o (T*k, D) are scratch.
 int few_max_tokens(const moe_dims_t& d);
 moe_status_t launch_few(const moe_dims_t& d, const uint16_t* x, const uint16_t* Wr, const uint16_t* br,
                         const moe_weight_t& W1, const uint16_t* b1, const moe_weight_t& W2, const uint16_t* b2,
-                        uint16_t* y, float* logits, uint16_t* h, float* o, unsigned* done, void* ws, cudaStream_t s);
+                        uint16_t* y, float* logits, uint16_t* h, float* o, void* ws, cudaStream_t s);
 
 // Grouped GEMMs (grouped_gemm.cu). Return MOE_OK or an error code.
 moe_status_t launch_mlp1(const moe_dims_t& d, const uint16_t* x_perm, const int32_t* offsets,

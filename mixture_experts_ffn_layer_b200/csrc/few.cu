@@ -13,8 +13,8 @@
 //      rows and the 8 up rows of W1), are split evenly over the blocks; h
 //      (bf16, rows by expert) goes to the workspace; grid barrier.
 //   3. mlp2: granules of 16 rows of W2, split the same way; the fp32 expert
-//      outputs go to the workspace, and the block that finishes the last
-//      expert of 16 output columns sums their k terms per token in slot order.
+//      outputs go to the workspace; grid barrier;
+//   4. combine: the k terms of every output element in slot order.
 //
 // A granule is 16 weight rows by the whole reduction. The block's 16 warps
 // split the reduction, so that every SM has work for as little as one token
@@ -66,9 +66,9 @@ constexpr int64_t kMaxRowBytes = 65536 * 2;  // T * max(D, I) bf16 of resident a
 constexpr uint64_t kBarrierNs = 1000000000ull;
 
 // Grid-barrier counters in the workspace header (the status word is at byte
-// 0), as 32-bit words: blocks that reached the first and the second barrier,
-// and blocks that are done.
-constexpr int kBar1 = 16, kBar2 = 24, kExit = 32;
+// 0), as 32-bit words: blocks that reached each of the barriers, and blocks that
+// are done.
+constexpr int kBar1 = 16, kBar2 = 24, kBar3 = 32, kExit = 40;
 
 // bf16 rings: a stage is 2 units of 32 of 16 rows, 128 bytes of a row, with
 // the 16-byte pieces swizzled by row parity.
@@ -84,7 +84,6 @@ struct FewParams {
   float* logits;     // (T, E)
   uint16_t* h;       // (T*k, I) bf16, rows by expert
   float* o;          // (T*k, D) fp32, by assignment, gate weight applied
-  unsigned* done;    // (D/16) expert granules finished
   uint16_t* y;
   unsigned* header;  // workspace header
   int stages;        // of a warp's bf16 ring, or of the block's MXFP4 ring
@@ -191,11 +190,12 @@ __device__ __forceinline__ void grid_barrier(unsigned* header, int which) {
 }
 
 // The last block to leave sets the counters back to zero for the next call
-// (every block has then passed both barriers, or given up on them).
+// (every block has then passed the barriers, or given up on them).
 __device__ __forceinline__ void grid_exit(unsigned* header) {
   if (threadIdx.x == 0 && atomicAdd(header + kExit, 1u) == gridDim.x - 1) {
     header[kBar1] = 0;
     header[kBar2] = 0;
+    header[kBar3] = 0;
     header[kExit] = 0;
   }
 }
@@ -231,7 +231,6 @@ struct FewShared {
   float dot[kWarps];
   uint32_t row_max[kMaxT];       // |largest| of each resident row (bf16 bits)
   float row_scale[kMaxT];        // what a resident row's sums are multiplied with
-  int last[kMaxActive];
 };
 
 // How many granules a block works on at a time, 16 / that many warps on each:
@@ -469,25 +468,32 @@ __device__ __forceinline__ void load_rows(const FewParams& p, FewShared& sh, con
                                           uint8_t* act) {
   const int per = K / 8;  // 16-byte chunks per row
   const int total = rows * per;
-  for (int base = threadIdx.x & ~31; base < total; base += kThreads) {  // (uniform in a warp)
-    const int i = base + (threadIdx.x & 31);
-    const bool on = i < total;
-    const int n = min(i, total - 1) / per, c = i - n * per;
-    uint32_t m = 0;
-    if (on) {
-      const uint4 v = __ldcg(reinterpret_cast<const uint4*>(from) + i);
-      *reinterpret_cast<uint4*>(act + n * p.row_pitch + c * 16) = v;
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  constexpr int kAtOnce = 4;  // loads in flight per thread
+  for (int base = threadIdx.x & ~31; base < total; base += kAtOnce * kThreads) {  // (uniform in a warp)
+    uint4 v[kAtOnce];
 #pragma unroll
-      for (int z = 0; z < 4; ++z) m = max(m, max(w[z] & 0x7fffu, (w[z] >> 16) & 0x7fffu));
+    for (int z = 0; z < kAtOnce; ++z) {
+      const int i = base + z * kThreads + (threadIdx.x & 31);
+      v[z] = i < total ? __ldcg(reinterpret_cast<const uint4*>(from) + i) : make_uint4(0, 0, 0, 0);
     }
-    if (kFmt == MOE_W_MXFP4) {
-      // a warp's chunks are consecutive: mostly of one row, then one atomic
-      if (__shfl_sync(0xffffffffu, n, 0) == __shfl_sync(0xffffffffu, n, 31)) {
-        m = __reduce_max_sync(0xffffffffu, m);
-        if ((threadIdx.x & 31) == 0) atomicMax(&sh.row_max[n], m);
-      } else if (on) {
-        atomicMax(&sh.row_max[n], m);
+#pragma unroll
+    for (int z = 0; z < kAtOnce; ++z) {
+      const int first = base + z * kThreads, i = first + (threadIdx.x & 31);
+      if (first >= total) break;
+      const int n = min(i, total - 1) / per, c = i - n * per;
+      if (i < total) *reinterpret_cast<uint4*>(act + n * p.row_pitch + c * 16) = v[z];
+      if (kFmt == MOE_W_MXFP4) {
+        const uint32_t w[4] = {v[z].x, v[z].y, v[z].z, v[z].w};
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = max(m, max(w[j] & 0x7fffu, (w[j] >> 16) & 0x7fffu));
+        // a warp's chunks are consecutive: mostly of one row, then one atomic
+        if (__shfl_sync(0xffffffffu, n, 0) == __shfl_sync(0xffffffffu, n, 31)) {
+          m = __reduce_max_sync(0xffffffffu, m);
+          if ((threadIdx.x & 31) == 0) atomicMax(&sh.row_max[n], m);
+        } else {
+          atomicMax(&sh.row_max[n], m);
+        }
       }
     }
   }
@@ -550,7 +556,7 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 : 0), 1) 
     }
   }
 
-  // ---- router logits; the tokens' rows; the completion counters start at zero
+  // ---- router logits; the tokens' rows
   if (threadIdx.x < 256) sh.tokens[threadIdx.x] = 0;
   if (threadIdx.x < kMaxT) sh.row_max[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
@@ -560,7 +566,6 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 : 0), 1) 
     }
     sm100::fence_mbar_init();
   }
-  for (int i = blockIdx.x * kThreads + threadIdx.x; i < p.D / 16; i += gridDim.x * kThreads) p.done[i] = 0;
   {
     // this block's logits, each by 16 / groups warps (one warp when there are
     // many), their parts added in warp order
@@ -858,29 +863,21 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 : 0), 1) 
   }
   cp_wait<0>();
 
-  // ---- combine: the block whose granule is the last of its 16 columns
-  warps_sync();
-  const int n2 = st2.g1 - st2.g0;
-  for (int base = 0; base < n2; base += kMaxActive) {
-    const int cnt = min(kMaxActive, n2 - base);
-    if (static_cast<int>(threadIdx.x) < cnt) {
-      const int dg = (st2.g0 + base + static_cast<int>(threadIdx.x)) % st2.per_expert;
-      __threadfence();
-      const bool last = atomicAdd(p.done + dg, 1u) == static_cast<unsigned>(n_active - 1);
-      __threadfence();
-      sh.last[threadIdx.x] = last ? dg : -1;
-    }
-    warps_sync();
-    const int per = p.T * 16;
-    for (int i = threadIdx.x; i < cnt * per; i += kThreads) {
-      const int dg = sh.last[i / per];
-      if (dg < 0) continue;
-      const int t = (i % per) / 16, d0 = dg * 16 + i % 16;
-      float v = 0.0f;
-      for (int j = 0; j < p.k; ++j) v += __ldcg(p.o + static_cast<int64_t>(t * p.k + j) * p.D + d0);
-      p.y[static_cast<int64_t>(t) * p.D + d0] = float_to_bf16_bits(v);
-    }
-    warps_sync();
+  // ---- combine: four columns of a token per thread, over the whole grid
+  grid_barrier(p.header, kBar3);
+  for (int i = blockIdx.x + threadIdx.x * gridDim.x; i < p.T * (p.D / 4); i += gridDim.x * kThreads) {
+    const int t = i / (p.D / 4), c = i % (p.D / 4);
+    const float4* from = reinterpret_cast<const float4*>(p.o + static_cast<int64_t>(t) * p.k * p.D) + c;
+    float4 v[kMaxK];
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j)
+      if (j < p.k) v[j] = __ldcg(from + static_cast<int64_t>(j) * (p.D / 4));
+    float4 sum = v[0];
+#pragma unroll
+    for (int j = 1; j < kMaxK; ++j)
+      if (j < p.k) sum = make_float4(sum.x + v[j].x, sum.y + v[j].y, sum.z + v[j].z, sum.w + v[j].w);
+    *reinterpret_cast<uint2*>(p.y + static_cast<int64_t>(t) * p.D + 4 * c) =
+        make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
   }
   grid_exit(p.header);
 }
@@ -927,7 +924,7 @@ int few_max_tokens(const moe_dims_t& d) {
 
 moe_status_t launch_few(const moe_dims_t& d, const uint16_t* x, const uint16_t* Wr, const uint16_t* br,
                         const moe_weight_t& W1, const uint16_t* b1, const moe_weight_t& W2, const uint16_t* b2,
-                        uint16_t* y, float* logits, uint16_t* h, float* o, unsigned* done, void* ws, cudaStream_t s) {
+                        uint16_t* y, float* logits, uint16_t* h, float* o, void* ws, cudaStream_t s) {
   FewParams p{};
   p.T = d.T;
   p.D = d.D;
@@ -946,7 +943,6 @@ moe_status_t launch_few(const moe_dims_t& d, const uint16_t* x, const uint16_t* 
   p.logits = logits;
   p.h = h;
   p.o = o;
-  p.done = done;
   p.y = y;
   p.header = static_cast<unsigned*>(ws);
   // rows 64 bytes off a multiple of 128: two rows' 64-byte pieces on distinct banks

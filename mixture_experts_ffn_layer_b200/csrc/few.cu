@@ -200,10 +200,23 @@ __device__ __forceinline__ void grid_exit(unsigned* header) {
   }
 }
 
+// Wait for a phase of an mbarrier, kBarrierNs at most. The clock is looked at
+// only now and then: reading it takes as long as these waits mostly last.
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; !sm100::mbar_try_wait(bar, parity); ++i) {
+    if ((i & 255u) == 0) {
+      const uint64_t now = sm100::globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kBarrierNs) return false;
+    }
+  }
+  return true;
+}
+
 // Wait inside the block for warps that are on their way.
 __device__ __forceinline__ void wait_local(uint32_t bar, uint32_t parity, unsigned* header) {
-  if (!sm100::mbar_wait_bounded(bar, parity, nullptr, kBarrierNs))
-    record_status(reinterpret_cast<int*>(header), MOE_ERR_TIMEOUT);
+  if (!wait_bounded(bar, parity)) record_status(reinterpret_cast<int*>(header), MOE_ERR_TIMEOUT);
 }
 
 // Order-preserving integer of a logit; NaN sorts below every number, -0 as +0.
@@ -368,7 +381,7 @@ __device__ __forceinline__ void mx_produce(const FewParams& p, FewShared& sh, co
       const uint8_t* w = (which == 1 ? p.w1 : p.w2) + row0 * st.row_bytes;
       const uint8_t* s = (which == 1 ? p.s1 : p.s2) + row0 * st.srow_bytes;
       for (int c = 0; c < st.nchunks; ++c) {
-        if (!mbar_wait_bounded(empty + 8 * slot, phase ^ 1u, nullptr, kBarrierNs)) {
+        if (!wait_bounded(empty + 8 * slot, phase ^ 1u)) {
           failed = true;
           break;
         }
@@ -402,7 +415,7 @@ __device__ __forceinline__ void mx_produce(const FewParams& p, FewShared& sh, co
         slot = p.stages - 1;
         phase ^= 1u;
       }
-      mbar_wait_bounded(full + 8 * slot, phase, nullptr, kBarrierNs);
+      wait_bounded(full + 8 * slot, phase);
     }
   }
 }

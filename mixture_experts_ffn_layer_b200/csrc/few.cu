@@ -47,6 +47,8 @@
 // reproducible.
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "sm100.cuh"
 #include "tma_host.cuh"
@@ -73,9 +75,8 @@ constexpr int kBar1 = 16, kBar2 = 24, kBar3 = 32, kExit = 40;
 // bf16 rings: a stage is 2 units of 32 of 16 rows, 128 bytes of a row, with
 // the 16-byte pieces swizzled by row parity.
 constexpr int kBfUnits = 2, kBfPitch = 128, kBfSlot = 16 * kBfPitch;
-// MXFP4 ring: a stage is a granule, or the part of it over at most
-// kMxChunkUnits units of the reduction.
-constexpr int kMxChunkUnits = 128;
+// MXFP4 ring: a stage is two neighbouring granules, or their part over a chunk
+// of the reduction where they are too large for it.
 
 struct FewParams {
   int T, D, E, k, I;
@@ -88,6 +89,7 @@ struct FewParams {
   unsigned* header;  // workspace header
   int stages;        // of a warp's bf16 ring, or of the block's MXFP4 ring
   int slab_bytes;    // MXFP4: a stage
+  int nchunks1, nchunks2;  // MXFP4: parts of the reduction of W1's and W2's stages
   int red_bufs;      // buffers for the warps' partial sums: 4, or 2 or 1 where shared memory is short
   int row_pitch;     // bytes between resident activation rows
   Act act;
@@ -246,15 +248,6 @@ struct FewShared {
   float row_scale[kMaxT];        // what a resident row's sums are multiplied with
 };
 
-// How many granules a block works on at a time, 16 / that many warps on each:
-// the more, the fewer partial sums meet and the longer each warp's slice; but
-// a block with few granules, or a short reduction, has too little for it.
-__device__ __forceinline__ int pick_sides(int granules) {
-  int sides = 1;
-  while (sides < 4 && granules >= 4 * sides) sides *= 2;
-  return sides;
-}
-
 // One weight's granules as this block and warp see them.
 struct Stream {
   int64_t row_bytes;     // of the weight
@@ -263,7 +256,8 @@ struct Stream {
   int up;                // row of the 9th weight row relative to the 1st (I: the up half; 8)
   int step;              // weight rows a granule advances by (8 or 16)
   int per_expert;        // granules per expert
-  int side, sides;       // this warp's granule of the `sides` that the block works on at a time
+  int turn;              // granules that the block works on at a time, kWarps / turn warps on each
+  int side;              // this warp's granule of them
   int u0, u1;            // this warp's units of 32 of the reduction
   int units;             // units of the reduction
   int nchunks;           // stages per granule
@@ -285,14 +279,14 @@ __device__ __forceinline__ Stream make_stream(const FewParams& p, int which, int
   const uint32_t n = n_active * s.per_expert;  // at most 128 * 2048
   s.g0 = static_cast<int>(n * blockIdx.x / gridDim.x);
   s.g1 = static_cast<int>(n * (blockIdx.x + 1) / gridDim.x);
-  s.sides = kFmt == MOE_W_MXFP4 ? pick_sides(n / gridDim.x) : 1;
-  const int split = kWarps / s.sides;
+  s.turn = kFmt == MOE_W_BF16 ? 1 : n / gridDim.x >= 4 ? 4 : 2;
+  const int split = kWarps / s.turn;
   s.side = warp / split;
-  // bf16: this warp's units, two a stage; MXFP4: stages of nearly equal parts
+  // bf16: this warp's units, two a stage
   const int per = (s.units + split - 1) / split;
   s.u0 = min(s.units, warp % split * per);
   s.u1 = min(s.units, s.u0 + per);
-  s.nchunks = kFmt == MOE_W_BF16 ? (per + kBfUnits - 1) / kBfUnits : (s.units + kMxChunkUnits - 1) / kMxChunkUnits;
+  s.nchunks = kFmt == MOE_W_BF16 ? (per + kBfUnits - 1) / kBfUnits : which == 1 ? p.nchunks1 : p.nchunks2;
   s.chunk = (s.units + s.nchunks - 1) / s.nchunks;
   return s;
 }
@@ -355,15 +349,21 @@ struct Loader {
 };
 
 // Bytes between a stage's rows of codes. Rows 32 or 96 bytes off a multiple of
-// 128 collide two ways at most and are copied as they lie, 8 at a time; others
+// 128 collide two ways at most and are copied as they lie, a granule's 8 or 16
+// at a time (a bulk copy costs its issuer some 60 ns whatever its size); others
 // are copied row by row to an odd multiple of 16 (no collision).
 __host__ __device__ constexpr bool mx_as_stored(int units, int nchunks) { return nchunks == 1 && units % 4 == 2; }
 __host__ __device__ constexpr int mx_pitch(int units, int nchunks, int chunk) {
   return mx_as_stored(units, nchunks) ? units * 16 : (chunk | 1) * 16;
 }
+// A stage: 32 rows of codes, then all of the 32 rows' scales (with every chunk).
+__host__ __device__ constexpr int mx_stage_bytes(int units, int nchunks) {
+  return (32 * (mx_pitch(units, nchunks, (units + nchunks - 1) / nchunks) + units) + 127) / 128 * 128;
+}
 
-// The loading warp of an MXFP4 block: every granule of the block in order,
-// mlp1's then mlp2's.
+// The loading warp of an MXFP4 block: mlp1's granules then mlp2's, turn by
+// turn, two granules a stage. Of W1 rows 0..15 of a stage are gate rows and
+// 16..31 the up rows.
 __device__ __forceinline__ void mx_produce(const FewParams& p, FewShared& sh, const Stream& st1, const Stream& st2,
                                            uint32_t ring, int lane) {
   using namespace sm100;
@@ -375,8 +375,12 @@ __device__ __forceinline__ void mx_produce(const FewParams& p, FewShared& sh, co
     const Stream& st = which == 1 ? st1 : st2;
     const int pitch = mx_pitch(st.units, st.nchunks, st.chunk);
     const bool as_stored = mx_as_stored(st.units, st.nchunks);
-    for (int g = st.g0; g < st.g1 && !failed; ++g) {
-      const int ai = g / st.per_expert, local = g % st.per_expert;
+    int ai = st.g0 / st.per_expert, local = st.g0 % st.per_expert, in_turn = 0;
+    for (int g = st.g0; g < st.g1 && !failed;) {
+      const int left = min(st.per_expert - local, st.g1 - g);  // of this expert
+      const int count = min(2, min(left, st.turn - in_turn));
+      // runs of neighbouring rows: W1's gate and up rows, W2's rows
+      const int runs = which == 1 ? 2 : 1, run = count * (which == 1 ? 8 : 16);
       const int64_t row0 = static_cast<int64_t>(sh.expert[ai]) * st.rows + static_cast<int64_t>(local) * st.step;
       const uint8_t* w = (which == 1 ? p.w1 : p.w2) + row0 * st.row_bytes;
       const uint8_t* s = (which == 1 ? p.s1 : p.s2) + row0 * st.srow_bytes;
@@ -387,23 +391,34 @@ __device__ __forceinline__ void mx_produce(const FewParams& p, FewShared& sh, co
         }
         const int n = min(st.chunk, st.units - c * st.chunk);
         const uint32_t bar = full + 8 * slot, to = ring + slot * p.slab_bytes;
-        if (lane == 0) mbar_arrive_expect_tx(bar, 16 * (n * 16 + st.srow_bytes));
+        if (lane == 0) mbar_arrive_expect_tx(bar, 16 * count * (n * 16 + st.srow_bytes));
         __syncwarp();
+        if (lane < runs)
+          bulk_load(to + 32 * pitch + lane * 16 * st.srow_bytes, s + static_cast<int64_t>(lane) * st.up * st.srow_bytes,
+                    run * st.srow_bytes, bar);
         if (as_stored) {
-          if (lane < 2) bulk_load(to + lane * 8 * pitch, w + lane * st.up * st.row_bytes, 8 * pitch, bar);
-        } else if (lane < 16) {
-          const int wr = lane < 8 ? lane : st.up + lane - 8;
-          bulk_load(to + lane * pitch, w + wr * st.row_bytes + c * st.chunk * 16, n * 16, bar);
+          if (lane < runs)
+            bulk_load(to + lane * 16 * pitch, w + lane * st.up * st.row_bytes, run * pitch, bar);
+        } else {
+          const int r = lane % run, wr = r + lane / run * st.up;  // (W2: lanes past its rows have none)
+          if (lane < runs * run)
+            bulk_load(to + (lane / run * 16 + r) * pitch, w + wr * st.row_bytes + c * st.chunk * 16, n * 16, bar);
         }
-        // all of the 16 rows' scales, with every stage of the granule
-        if (lane == 16 || lane == 17)
-          bulk_load(to + 16 * pitch + (lane - 16) * 8 * st.srow_bytes,
-                    s + static_cast<int64_t>(lane - 16) * st.up * st.srow_bytes, 8 * st.srow_bytes, bar);
         ++issued;
         if (++slot == p.stages) {
           slot = 0;
           phase ^= 1u;
         }
+      }
+      g += count;
+      local += count;
+      in_turn += count;
+      if (local == st.per_expert) {
+        local = 0;
+        ++ai;
+        in_turn = 0;
+      } else if (in_turn == st.turn) {
+        in_turn = 0;
       }
     }
   }
@@ -722,7 +737,7 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 : 0), 1) 
     const Stream& s = which == 1 ? st1 : st2;
     if (which == 2) grid_barrier(p.header, kBar2);  // h is complete
     const int pitch = mx_pitch(s.units, s.nchunks, s.chunk);
-    const int split = kWarps / s.sides, tasks = s.sides * 4 * kN;
+    const int split = kWarps / s.turn, tasks = s.turn * 4 * kN;
     for (int ai = s.g0 / s.per_expert; s.g0 < s.g1 && ai * s.per_expert < s.g1; ++ai) {
       const int begin = max(0, s.g0 - ai * s.per_expert), end = min(s.per_expert, s.g1 - ai * s.per_expert);
       const int e = sh.expert[ai], start = sh.start[ai], rows = sh.start[ai + 1] - start;
@@ -797,7 +812,7 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 : 0), 1) 
           }
         }
       };
-      for (int base = begin; base < end; base += s.sides, ++it) {
+      for (int base = begin; base < end; base += s.turn, ++it) {
         float acc[kN][4];
 #pragma unroll
         for (int i = 0; i < kN; ++i)
@@ -818,30 +833,30 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 : 0), 1) 
           }
         } else {
           // Every warp waits for every stage of the turn, in order, and frees
-          // it -- at once where the stage belongs to another side -- so that no
-          // slot's phase passes a warp by.
-          const int mine = s.side * s.nchunks, all = min(s.sides, end - base) * s.nchunks;
-          for (int i = 0; i < all; ++i) {
+          // it -- at once where its granule is not in it -- so that no slot's
+          // phase passes a warp by.
+          const int count = min(s.turn, end - base);
+          for (int i = 0; i < (count + 1) / 2 * s.nchunks; ++i) {
             wait_local(sm100::smem_u32(&sh.w_full[slot]), slab_phase, p.header);
-            const int chunk = i - mine;
-            if (chunk >= 0 && chunk < s.nchunks) {
+            const int chunk = i - s.side / 2 * s.nchunks;
+            if (chunk >= 0 && chunk < s.nchunks && s.side < count) {
               // this warp's units of the stage
               const int first = chunk * s.chunk, n = min(s.chunk, s.units - first), per = (n + split - 1) / split;
               const int u0 = min(n, warp % split * per);
               int left = min(n, u0 + per) - u0;
-              const uint8_t* at = ring + slot * p.slab_bytes + fr * pitch + u0 * 16 + fq * 4;
-              const uint8_t* at8 = at + 8 * pitch;
-              const uint8_t* s_lo = ring + slot * p.slab_bytes + 16 * pitch + fr * s.srow_bytes + first + u0;
-              const uint8_t* s_hi = s_lo + 8 * s.srow_bytes;
+              const uint8_t* slab = ring + slot * p.slab_bytes;
+              const int lo = (which == 1 ? 8 : 16) * (s.side & 1) + fr, hi = lo + (which == 1 ? 16 : 8);  // its rows
+              const uint8_t* at = slab + lo * pitch + u0 * 16 + fq * 4;
+              const uint8_t* at8 = at + (hi - lo) * pitch;
+              const uint8_t* s_lo = slab + 32 * pitch + lo * s.srow_bytes + first + u0;
+              const uint8_t* s_hi = s_lo + (hi - lo) * s.srow_bytes;
               const uint8_t* b[kN];
 #pragma unroll
               for (int j = 0; j < kN; ++j) b[j] = brow[j] + (first + u0) * 64;
               for (; left >= 8; left -= 8) mul_mx<kN, 8>(at, at8, s_lo, s_hi, b, acc);
-              if (left >= 4) {
-                mul_mx<kN, 4>(at, at8, s_lo, s_hi, b, acc);
-                left -= 4;
-              }
-              for (; left > 0; --left) mul_mx<kN, 1>(at, at8, s_lo, s_hi, b, acc);
+              if (left & 4) mul_mx<kN, 4>(at, at8, s_lo, s_hi, b, acc);
+              if (left & 2) mul_mx<kN, 2>(at, at8, s_lo, s_hi, b, acc);
+              if (left & 1) mul_mx<kN, 1>(at, at8, s_lo, s_hi, b, acc);
             }
             __syncwarp();
             if (lane == 0) sm100::mbar_arrive(sm100::smem_u32(&sh.w_empty[slot]));
@@ -867,11 +882,11 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 : 0), 1) 
           load_bias(base, it);
           finish(base, it);
         } else {
-          if (base > begin) finish(base - s.sides, it - 1);
+          if (base > begin) finish(base - s.turn, it - 1);
           load_bias(base, it);
         }
       }
-      if (p.red_bufs > 1) finish(begin + (end - begin - 1) / s.sides * s.sides, it - 1);
+      if (p.red_bufs > 1) finish(begin + (end - begin - 1) / s.turn * s.turn, it - 1);
     }
   }
   cp_wait<0>();
@@ -899,17 +914,20 @@ template <int kFmt, int kN>
 moe_status_t launch(FewParams p, cudaStream_t s) {
   constexpr bool mx = kFmt == MOE_W_MXFP4;
   const int red = kWarps * 128 * kN * 4;
+  const int room = kMaxSmem - 4096 - p.T * p.row_pitch;
   if (mx) {
-    for (const int K : {p.D, p.I}) {
-      const int units = K / 32, nchunks = (units + kMxChunkUnits - 1) / kMxChunkUnits;
-      const int bytes = 16 * (mx_pitch(units, nchunks, (units + nchunks - 1) / nchunks) + units);
-      if (bytes > p.slab_bytes) p.slab_bytes = (bytes + 127) / 128 * 128;
+    // as few parts of the reduction as let two stages fit
+    for (int which = 1; which <= 2; ++which) {
+      const int units = (which == 1 ? p.D : p.I) / 32;
+      int nchunks = 1;
+      while (2 * mx_stage_bytes(units, nchunks) > room - red && nchunks < units) ++nchunks;
+      (which == 1 ? p.nchunks1 : p.nchunks2) = nchunks;
+      p.slab_bytes = std::max(p.slab_bytes, mx_stage_bytes(units, nchunks));
     }
   }
   const int stage = mx ? p.slab_bytes : kWarps * kBfSlot;
   // the partial sums' buffers after two stages, then as many stages as fit
-  const int room = kMaxSmem - 4096 - p.T * p.row_pitch;
-  p.red_bufs = kN == 1 && room - 4 * red >= 2 * stage ? 4 : room - 2 * red >= 2 * stage ? 2 : 1;
+  p.red_bufs = kN == 1 && room - 4 * red >= 3 * stage ? 4 : room - 2 * red >= 2 * stage ? 2 : 1;
   int stages = (room - p.red_bufs * red) / stage;
   if (stages > kMaxStages) stages = kMaxStages;
   if (stages < 2) return MOE_ERR_UNSUPPORTED;

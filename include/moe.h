@@ -259,6 +259,39 @@ typedef struct {
 MOE_API moe_status_t moe_rmsnorm(moe_norm_t n, const uint16_t* x, const void* residual, const uint16_t* gamma,
                          void* res_out, uint16_t* y, uint8_t* q, float* q_scale, void* stream);
 
+/* R rows, E weight matrices of N output columns, reduction length K, type of
+ * the output (moe_type_t). */
+typedef struct {
+  int32_t R, E, N, K;
+  int32_t out_type;
+} moe_fp8_t;
+
+/* Matrix product in 8-bit floating point with a scale for each block of 128,
+ * dense or grouped by expert: beside moe_mlp1 / moe_mlp2 for weights kept in
+ * E4M3 with 128 x 128 block scales, and for dense projections (E = 1).
+ * Defined by: torchtitan GPT-OSS guide, "grouped matrix multiplication" (the
+ * grouped GEMM over expert segments, and its FP8 converter option); the block
+ * scales are this library's reading of it.
+ *   for r in [offsets[e], offsets[e+1]):
+ *   out[r,n] = bias[e,n] + sum over the blocks b of 128 k of
+ *              a_scale[r,b] * w_scale[e,n/128,b] * (sum of a[r,k] * w[e,n,k] over the block)
+ *   a (R,K) E4M3, a_scale (R, ceil(K/128)) fp32 (as moe_rmsnorm writes them);
+ *   w (E,N,K) E4M3, w_scale (E, ceil(N/128), ceil(K/128)) fp32;
+ *   offsets (E+1) int32 on the device, ascending from 0 (NULL for E = 1: all
+ *   rows); bias (E,N) bf16 or NULL -> out (R,N) bf16 or fp32. Rows from
+ *   offsets[E] on are left as they are.
+ * Products are summed in fp32 within a block (tensor cores) and over the
+ * blocks; one rounding to bf16 at the end. Deterministic for given sizes.
+ * R >= 0 (R = 0: nothing is enqueued), E <= 256, N and K multiples of 16 up to
+ * 65536. ws: at least moe_fp8_workspace_bytes(d) (the device status word; any
+ * workspace of this library is large enough). Offsets that do not ascend
+ * within [0, R] record MOE_ERR_DEVICE_BOUNDS and write nothing. */
+MOE_API moe_status_t moe_check_fp8(moe_fp8_t d);
+MOE_API size_t moe_fp8_workspace_bytes(moe_fp8_t d);
+MOE_API moe_status_t moe_fp8_matmul(moe_fp8_t d, const uint8_t* a, const float* a_scale, const int32_t* offsets,
+                            const uint8_t* w, const float* w_scale, const uint16_t* bias, void* out, void* ws,
+                            size_t ws_bytes, void* stream);
+
 /* The MXFP4 expert weights are multiplied as stored (E2M1 codes with E8M0
  * block scales, GPT-OSS in Transformers blog, MXFP4 paragraph) on block-scaled
  * tensor-core MMAs, which read the scales in their own layout: each MXFP4 GEMM

@@ -17,9 +17,10 @@ from ._binding import (  # noqa: F401
     moe_route, moe_permute, moe_gather, moe_mlp1, moe_mlp2, moe_ffn_grouped, moe_combine, moe_forward,
     moe_read_device_status, status_str, moe_permute_noalloc, moe_selftest_wait_timeout, mxfp4_prepared_bytes,
     moe_mxfp4_prepare, mxfp4_prepare, MOE_T_BF16, MOE_T_F32, NormDims, moe_forward_few, few_max_tokens, moe_rmsnorm,
+    Fp8Dims, fp8_dims, fp8_workspace_bytes, alloc_fp8_workspace, moe_fp8_matmul,
 )
 from .ep import CudaLocalOps, ExpertParallelMoE, ep_forward  # noqa: F401,E402
-from .block import MoEBlock, rmsnorm, rmsnorm_fp8  # noqa: F401,E402
+from .block import MoEBlock, fp8_matmul, rmsnorm, rmsnorm_fp8  # noqa: F401,E402
 
 
 class MoELayer:

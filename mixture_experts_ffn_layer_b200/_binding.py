@@ -26,7 +26,8 @@ STATUS = {
 EXPORTS = ("moe_workspace_bytes", "moe_check_dims", "moe_route", "moe_permute", "moe_gather", "moe_mlp1", "moe_mlp2",
            "moe_ffn_grouped", "moe_combine", "moe_forward", "moe_read_device_status", "moe_status_str",
            "moe_permute_noalloc", "moe_selftest_wait_timeout", "moe_mxfp4_prepared_bytes", "moe_mxfp4_prepare",
-           "moe_forward_few", "moe_few_max_tokens", "moe_rmsnorm")
+           "moe_forward_few", "moe_few_max_tokens", "moe_rmsnorm", "moe_check_fp8", "moe_fp8_workspace_bytes",
+           "moe_fp8_matmul")
 
 
 class MoeError(RuntimeError):
@@ -48,6 +49,11 @@ class Weight(ctypes.Structure):
 class NormDims(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("D", ctypes.c_int32), ("ldx", ctypes.c_int64), ("eps", ctypes.c_float),
                 ("res_type", ctypes.c_int32)]
+
+
+class Fp8Dims(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int32), ("E", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("out_type", ctypes.c_int32)]
 
 
 _lib = None
@@ -85,6 +91,9 @@ def load(path: str = LIB_PATH):
         "moe_forward_few": (ctypes.c_int, [Dims, VP, VP, VP, Weight, VP, Weight, VP, VP, VP, ctypes.c_size_t, VP]),
         "moe_few_max_tokens": (ctypes.c_int32, [Dims]),
         "moe_rmsnorm": (ctypes.c_int, [NormDims, VP, VP, VP, VP, VP, VP, VP, VP]),
+        "moe_check_fp8": (ctypes.c_int, [Fp8Dims]),
+        "moe_fp8_workspace_bytes": (ctypes.c_size_t, [Fp8Dims]),
+        "moe_fp8_matmul": (ctypes.c_int, [Fp8Dims, VP, VP, VP, VP, VP, VP, VP, VP, ctypes.c_size_t, VP]),
         "moe_mxfp4_prepare": (ctypes.c_int, [Dims, ctypes.c_int32, Weight, VP, ctypes.c_size_t, VP]),
     }
     for name, (res, args) in sig.items():
@@ -190,6 +199,26 @@ def few_max_tokens(d: Dims) -> int:
 def moe_rmsnorm(n: NormDims, x, residual, gamma, res_out, y, q, q_scale, stream=None):
     _check(load().moe_rmsnorm(n, _p(x), _p(residual), _p(gamma), _p(res_out), _p(y), _p(q), _p(q_scale),
                               _stream(stream)), "moe_rmsnorm")
+
+
+def fp8_dims(R, E, N, K, out_dtype=torch.bfloat16) -> Fp8Dims:
+    return Fp8Dims(R, E, N, K, MOE_T_F32 if out_dtype == torch.float32 else MOE_T_BF16)
+
+
+def fp8_workspace_bytes(d: Fp8Dims) -> int:
+    n = load().moe_fp8_workspace_bytes(d)
+    if n == 0:
+        raise MoeError(load().moe_check_fp8(d), "moe_fp8_workspace_bytes")
+    return n
+
+
+def alloc_fp8_workspace(d: Fp8Dims, device="cuda") -> torch.Tensor:
+    return torch.zeros(fp8_workspace_bytes(d), dtype=torch.uint8, device=device)
+
+
+def moe_fp8_matmul(d: Fp8Dims, a, a_scale, offsets, w, w_scale, bias, out, ws, stream=None):
+    _check(load().moe_fp8_matmul(d, _p(a), _p(a_scale), _p(offsets), _p(w), _p(w_scale), _p(bias), _p(out), _p(ws),
+                                 ws.numel(), _stream(stream)), "moe_fp8_matmul")
 
 
 def moe_permute_noalloc(d, topk_idx, counts, offsets, perm, inv, stream=None):

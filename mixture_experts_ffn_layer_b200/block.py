@@ -60,6 +60,36 @@ def rmsnorm_fp8(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-5, residua
     return q, scale, res
 
 
+def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, ws: torch.Tensor,
+               offsets: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               out: Optional[torch.Tensor] = None, out_dtype=BF16, stream=None) -> torch.Tensor:
+    """The block-scaled FP8 product (moe_fp8_matmul): a (R, K) and w (E, N, K)
+    E4M3, a_scale (R, ceil(K/128)) and w_scale (E, ceil(N/128), ceil(K/128))
+    fp32, as rmsnorm_fp8 gives the left operand. With ``offsets`` (E+1) int32
+    the rows of [offsets[e], offsets[e+1]) are multiplied with w[e]; without,
+    E = 1 and all rows are. ``bias`` (E, N) bf16. Returns (R, N)."""
+    _require(a.dim() == 2 and w.dim() == 3 and a.shape[1] == w.shape[2], "a must be (R, K) and w (E, N, K)")
+    R, K = a.shape
+    E, N, _ = w.shape
+    kb, nb = -(-K // 128), -(-N // 128)
+    _require(a.dtype == torch.float8_e4m3fn and w.dtype == torch.float8_e4m3fn, "a and w must be float8_e4m3fn")
+    _require(a_scale.shape == (R, kb) and w_scale.shape == (E, nb, kb) and a_scale.dtype == torch.float32 and
+             w_scale.dtype == torch.float32, "a_scale must be (R, K/128) and w_scale (E, N/128, K/128) fp32")
+    _require(offsets is not None or E == 1, "E > 1 needs offsets")
+    _require(offsets is None or (offsets.shape == (E + 1,) and offsets.dtype == torch.int32),
+             "offsets must be (E+1,) int32")
+    _require(bias is None or (bias.shape == (E, N) and bias.dtype == BF16), "bias must be (E, N) bf16")
+    if out is None:
+        _require(out_dtype in (BF16, torch.float32), "out_dtype must be bf16 or fp32")
+        out = torch.empty((R, N), dtype=out_dtype, device=a.device)
+    _require(out.shape == (R, N) and out.dtype in (BF16, torch.float32), "out must be (R, N) bf16 or fp32")
+    for t in (a, a_scale, w, w_scale, ws, offsets, bias, out):
+        _require(t is None or (t.is_contiguous() and t.device == a.device), "tensors must be contiguous and on one device")
+    with torch.cuda.device(a.device):
+        B.moe_fp8_matmul(B.fp8_dims(R, E, N, K, out.dtype), a, a_scale, offsets, w, w_scale, bias, out, ws, stream)
+    return out
+
+
 class MoEBlock:
     """The feed-forward half of a transformer block: residual addition,
     RMSNorm and the MoE layer. ``forward(x, residual)`` returns (y, s) with

@@ -295,6 +295,29 @@ moe_status_t moe_rmsnorm(moe_norm_t n, const uint16_t* x, const void* residual, 
       launch_rmsnorm(n, x, residual, gamma, res_out, y, q, q_scale, static_cast<cudaStream_t>(stream)));
 }
 
+moe_status_t moe_check_fp8(moe_fp8_t d) {
+  if (d.R < 0 || d.E <= 0 || d.N <= 0 || d.K <= 0) return MOE_ERR_INVALID_ARG;
+  if (d.out_type != MOE_T_BF16 && d.out_type != MOE_T_F32) return MOE_ERR_INVALID_ARG;
+  if (d.E > 256 || d.N % 16 || d.K % 16 || d.N > 65536 || d.K > 65536) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+size_t moe_fp8_workspace_bytes(moe_fp8_t d) { return moe_check_fp8(d) == MOE_OK ? kWsHeader : 0; }
+
+moe_status_t moe_fp8_matmul(moe_fp8_t d, const uint8_t* a, const float* a_scale, const int32_t* offsets,
+                            const uint8_t* w, const float* w_scale, const uint16_t* bias, void* out, void* ws,
+                            size_t ws_bytes, void* stream) {
+  MOE_TRY(moe_check_fp8(d));
+  if (d.R == 0) return MOE_OK;
+  MOE_REQUIRE(a && a_scale && w && w_scale && out && (offsets || d.E == 1));
+  MOE_REQUIRE(aligned32(a) && aligned32(a_scale) && aligned32(offsets) && aligned32(w) && aligned32(w_scale) &&
+              aligned32(bias) && aligned32(out));
+  MOE_REQUIRE(ws && aligned32(ws));
+  if (ws_bytes < moe_fp8_workspace_bytes(d)) return MOE_ERR_WORKSPACE;
+  return launch_fp8_matmul(d, a, a_scale, offsets, w, w_scale, bias, out, status_word(ws),
+                           static_cast<cudaStream_t>(stream));
+}
+
 size_t moe_mxfp4_prepared_bytes(moe_dims_t d, int32_t which) {
   if (moe_check_dims(d) != MOE_OK || d.wfmt != MOE_W_MXFP4 || (which != 1 && which != 2)) return 0;
   return mx_prepared_bytes(d, which);

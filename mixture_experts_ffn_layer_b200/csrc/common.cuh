@@ -90,6 +90,11 @@ moe_status_t launch_few(const moe_dims_t& d, const uint16_t* x, const uint16_t* 
                         const moe_weight_t& W1, const uint16_t* b1, const moe_weight_t& W2, const uint16_t* b2,
                         uint16_t* y, float* logits, uint16_t* h, float* o, void* ws, cudaStream_t s);
 
+// Block-scaled FP8 matrix product (fp8_gemm.cu).
+moe_status_t launch_fp8_matmul(const moe_fp8_t& d, const uint8_t* a, const float* a_scale, const int32_t* offsets,
+                               const uint8_t* w, const float* w_scale, const uint16_t* bias, void* out, int* status,
+                               cudaStream_t s);
+
 // Grouped GEMMs (grouped_gemm.cu). Return MOE_OK or an error code.
 moe_status_t launch_mlp1(const moe_dims_t& d, const uint16_t* x_perm, const int32_t* offsets,
                          const uint16_t* W1, const uint16_t* b1, uint16_t* h, int* status, cudaStream_t s);

@@ -1,0 +1,405 @@
+// Block-scaled FP8 matrix product, dense or grouped by expert:
+//
+//   out[r, n] = sum_b a_scale[r, b] * w_scale[e, n / 128, b] *
+//               (sum of a[r, k] * w[e, n, k] over the 128 k of block b) + bias[e, n]
+//
+// for the rows r of expert e's segment, a and w in E4M3. The scales vary with
+// the block of the reduction, so a block's products are summed by the tensor
+// cores (tcgen05 kind::f8f6f4, fp32 in TMEM) and added to the running sum with
+// its scale by ordinary fp32 FMAs, out of TMEM into registers: one FMA per
+// output element and block, which at N = 256 takes eight warps about two
+// thirds of the time the tensor core needs for the block, and overlaps it in
+// the other of two TMEM buffers.
+//
+// One persistent block per SM over tiles of 128 rows x kBN columns:
+//   warp 0      TMA producer: the tile's 128 x 128 block of a (a box of 32
+//               rows where the tile has no more) and kBN x 128 block of w;
+//   warp 1      allocates TMEM, issues the four K = 32 MMAs of a block;
+//   warps 2..9  eight warps, one row and half of the columns per thread: keep
+//               the running sums in registers and write the output.
+// Tiles are numbered expert by expert, column tile, then row tile, from the
+// offsets on the device, as in the bf16 GEMM. All waits are bounded; on a
+// timeout the kernel records it, drains what is in flight and returns.
+#include "common.cuh"
+#include "gemm_common.cuh"
+#include "sm100.cuh"
+#include "tma_host.cuh"
+
+namespace moe {
+namespace {
+
+using namespace sm100;
+
+constexpr int BM = 128;
+constexpr int BK = 128;               // one scale block, one 128-byte swizzle row of E4M3
+constexpr int kSmallRows = 32;        // box of a for tiles with at most this many rows
+constexpr int kThreads = 320;
+constexpr int kMaxStages = 8;
+constexpr int kABytes = BM * BK;
+constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr int kCtrlBytes = 256;
+constexpr size_t kMaxSmem = 232448;
+
+struct Fp8Params {
+  int R, E, N, K, KB, NB, NT;  // blocks of K, blocks of N, column tiles
+  int stages;
+  int out_f32;
+  const float* a_scale;
+  const float* w_scale;
+  const int32_t* offsets;
+  const uint16_t* bias;
+  void* out;
+  int* status;
+};
+
+// kind::f8f6f4, A = B = E4M3, D = fp32, both K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+template <int kBN>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
+                    const __grid_constant__ CUtensorMap tmB, const Fp8Params p) {
+  constexpr int kCols = kBN / 2;             // columns per thread
+  constexpr int kLd = 16;                    // of them per TMEM load
+  constexpr uint32_t kTmemCols = 2 * kBN < 32 ? 32 : 2 * kBN;
+  constexpr uint32_t kStageBytes = kABytes + kBN * BK;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int S = p.stages;
+  uint8_t* ctrl = smem + S * kStageBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ctrl);  // full[8] empty[8] tfull[2] tempty[2] done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * (2 * kMaxStages + 5));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* bad_s = reinterpret_cast<int*>(tmem_slot + 2);
+  int* seg = reinterpret_cast<int*>(ctrl + kCtrlBytes);  // E+1 segment starts
+  int* tpre = seg + (p.E + 1);                           // E+1 tile prefix
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t bar0 = smem_u32(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
+  auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * kMaxStages + b); };
+  auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * kMaxStages + 2 + b); };
+  const uint32_t done_bar = bar0 + 8u * (2 * kMaxStages + 4);
+
+  // ---- prologue: segment table, tile prefix, barriers, TMEM
+  if (threadIdx.x == 0) {
+    *bad_s = 0;
+    *abort_flag = 0;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e <= p.E; e += blockDim.x) {
+    const int o = p.offsets ? p.offsets[e] : e * p.R;
+    seg[e] = o;
+    if (o < 0 || o > p.R || (e == 0 && o != 0)) atomicOr(bad_s, 1);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const int per = (p.E + 31) / 32;
+    const int e0 = lane * per;
+    int local = 0;
+    for (int e = e0; e < e0 + per && e < p.E; ++e) {
+      const int cnt = seg[e + 1] - seg[e];
+      if (cnt < 0) atomicOr(bad_s, 1);
+      local += cnt > 0 ? (cnt + BM - 1) / BM * p.NT : 0;
+    }
+    int incl = local;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += v;
+    }
+    int run = incl - local;
+    for (int e = e0; e < e0 + per && e < p.E; ++e) {
+      tpre[e] = run;
+      const int cnt = seg[e + 1] - seg[e];
+      run += cnt > 0 ? (cnt + BM - 1) / BM * p.NT : 0;
+    }
+    if (lane == 31) tpre[p.E] = incl;
+    __syncwarp();
+    if (lane == 0) {
+      if (*bad_s) {
+        record_status(p.status, MOE_ERR_DEVICE_BOUNDS);
+        tpre[p.E] = 0;
+      }
+      for (int s = 0; s < S; ++s) {
+        mbar_init(full_bar(s), 1);
+        mbar_init(empty_bar(s), 1);
+      }
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(tfull_bar(b), 1);
+        mbar_init(tempty_bar(b), 8);
+      }
+      mbar_init(done_bar, 1);
+      fence_mbar_init();
+      tma_prefetch_desc(&tmA);
+      tma_prefetch_desc(&tmA32);
+      tma_prefetch_desc(&tmB);
+    }
+  } else if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int total = tpre[p.E];
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------------------------------------------------- producer
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      bool failed = false;
+      for (int tile = blockIdx.x; tile < total && !failed; tile += gridDim.x) {
+        int e, nt, mt;
+        decode_tile(tile, tpre, seg, p.E, BM, e, nt, mt);
+        const int row0 = seg[e] + mt * BM;
+        const bool small = seg[e + 1] - row0 <= kSmallRows;
+        const CUtensorMap* ta = small ? &tmA32 : &tmA;
+        const uint32_t bytes = (small ? kSmallRows * BK : kABytes) + kBN * BK;
+        const int brow = e * p.N + nt * kBN;
+        for (int kb = 0; kb < p.KB; ++kb) {
+          if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, kWaitNs)) {
+            failed = true;
+            break;
+          }
+          const uint32_t a_dst = smem_u32(smem + stage * kStageBytes);
+          mbar_arrive_expect_tx(full_bar(stage), bytes);
+          tma_load_2d(a_dst + kABytes, &tmB, full_bar(stage), kb * BK, brow);
+          tma_load_2d(a_dst, ta, full_bar(stage), kb * BK, row0);
+          ++issued;
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (failed) {
+        record_status(p.status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+        // let the copies still in flight land before the CTA can exit
+        for (int i = issued < S ? issued : S; i > 0; --i) {
+          if (--stage < 0) {
+            stage = S - 1;
+            phase ^= 1u;
+          }
+          mbar_wait_bounded(full_bar(stage), phase, nullptr, kWaitNs);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---------------------------------------------------------- MMA issuer
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, buf_phase = 0;
+      bool failed = false;
+      for (int tile = blockIdx.x; tile < total && !failed; tile += gridDim.x) {
+        int e, nt, mt;
+        decode_tile(tile, tpre, seg, p.E, BM, e, nt, mt);
+        const uint32_t idesc = idesc_e4m3_f32(BM, min(kBN, p.N - nt * kBN));
+        for (int kb = 0; kb < p.KB; ++kb) {
+          if (!mbar_wait_bounded(tempty_bar(buf), buf_phase ^ 1u, abort_flag, kWaitNs) ||
+              !mbar_wait_bounded(full_bar(stage), phase, abort_flag, kWaitNs)) {
+            failed = true;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d_tmem = tmem_base + buf * kBN;
+          const uint32_t a_addr = smem_u32(smem + stage * kStageBytes);
+          const uint32_t b_addr = a_addr + kABytes;
+#pragma unroll
+          for (int kk = 0; kk < BK / 32; ++kk)
+            mma_f8(d_tmem, desc_kmajor_sw128(a_addr + kk * 32), desc_kmajor_sw128(b_addr + kk * 32), idesc,
+                   kk != 0 ? 1u : 0u);
+          tc_commit(empty_bar(stage));
+          tc_commit(tfull_bar(buf));
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if (++buf == 2) {
+            buf = 0;
+            buf_phase ^= 1u;
+          }
+        }
+      }
+      if (failed) {
+        record_status(p.status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      // all MMAs issued by this thread complete before TMEM is released
+      tc_commit(done_bar);
+      mbar_wait_bounded(done_bar, 0, nullptr, kWaitNs);
+    }
+  } else {
+    // ------------------------------------------------- running sums and output
+    const int q = warp & 3;            // TMEM lane quarter this warp may access
+    const int half = (warp - 2) / 4;   // its half of the columns
+    int buf = 0;
+    uint32_t buf_phase = 0;
+    bool failed = false;
+    for (int tile = blockIdx.x; tile < total && !failed; tile += gridDim.x) {
+      int e, nt, mt;
+      decode_tile(tile, tpre, seg, p.E, BM, e, nt, mt);
+      const int row = seg[e] + mt * BM + q * 32 + lane;
+      const bool valid = row < seg[e + 1];
+      const int n0 = nt * kBN + half * kCols;
+      // (a row past the segment repeats its last one's scales; nothing of it is written)
+      const float* sa = p.a_scale + static_cast<int64_t>(valid ? row : seg[e + 1] - 1) * p.KB;
+      const float* sw = p.w_scale + (static_cast<int64_t>(e) * p.NB + min(n0 / 128, p.NB - 1)) * p.KB;
+      float acc[kCols];
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) acc[c] = 0.0f;
+      float s_next = __ldg(sa) * __ldg(sw);
+      for (int kb = 0; kb < p.KB; ++kb) {
+        const float s = s_next;
+        if (kb + 1 < p.KB) s_next = __ldg(sa + kb + 1) * __ldg(sw + kb + 1);
+        const bool ok = mbar_wait_bounded(tfull_bar(buf), buf_phase, abort_flag, kWaitNs);
+        if (!__all_sync(0xffffffffu, ok)) {
+          failed = true;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t from = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kBN + half * kCols;
+#pragma unroll
+        for (int c = 0; c < kCols; c += kLd) {
+          uint32_t v[kLd];
+          tmem_ld_x8(from + c, v);
+          tmem_ld_x8(from + c + 8, v + 8);
+          tmem_ld_wait();
+          if (c + kLd == kCols) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tempty_bar(buf));
+          }
+#pragma unroll
+          for (int i = 0; i < kLd; ++i) acc[c + i] = fmaf(s, __uint_as_float(v[i]), acc[c + i]);
+        }
+        if (++buf == 2) {
+          buf = 0;
+          buf_phase ^= 1u;
+        }
+      }
+      if (failed) {
+        if (lane == 0) {
+          record_status(p.status, MOE_ERR_TIMEOUT);
+          *abort_flag = 1;
+        }
+        break;
+      }
+#pragma unroll
+      for (int c = 0; c < kCols; c += 16) {
+        if (n0 + c >= p.N) break;  // (uniform; N is a multiple of 16)
+        if (p.bias) {
+          const uint4* b = reinterpret_cast<const uint4*>(p.bias + static_cast<int64_t>(e) * p.N + n0 + c);
+          float f[8];
+          unpack8(__ldg(b), f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[c + i] += f[i];
+          unpack8(__ldg(b + 1), f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[c + 8 + i] += f[i];
+        }
+        if (!valid) continue;
+        const int64_t at = static_cast<int64_t>(row) * p.N + n0 + c;
+        if (p.out_f32) {
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = acc[c + i];
+          st_global_v8f(static_cast<float*>(p.out) + at, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = acc[c + 8 + i];
+          st_global_v8f(static_cast<float*>(p.out) + at + 8, v);
+        } else {
+          uint32_t v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = pack_bf16x2(acc[c + 2 * i], acc[c + 2 * i + 1]);
+          st_global_v8u(static_cast<uint16_t*>(p.out) + at, v);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, kTmemCols);
+  }
+}
+
+// 2-D tensor of `rows` rows of `inner` bytes, loaded in boxes of 128 bytes x
+// box_rows rows with the 128-byte swizzle; elements outside read as zero.
+bool make_tmap_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows) {
+  auto fn = tma_encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {inner, rows};
+  cuuint64_t strides[1] = {inner};
+  cuuint32_t box[2] = {BK, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kBN>
+moe_status_t launch(Fp8Params p, const uint8_t* a, const uint8_t* w, cudaStream_t s) {
+  CUtensorMap ta, ta32, tb;
+  if (!make_tmap_u8(&ta, a, p.K, p.R, BM) || !make_tmap_u8(&ta32, a, p.K, p.R, kSmallRows) ||
+      !make_tmap_u8(&tb, w, p.K, static_cast<uint64_t>(p.E) * p.N, kBN))
+    return MOE_ERR_CUDA;
+  constexpr size_t stage = kABytes + kBN * BK;
+  const size_t fixed = 1024 + kCtrlBytes + 2 * (p.E + 1) * sizeof(int);
+  p.stages = static_cast<int>((kMaxSmem - fixed) / stage);
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  p.NT = (p.N + kBN - 1) / kBN;
+  const size_t smem = fixed + p.stages * stage;
+  if (cudaFuncSetAttribute(fp8_gemm_kernel<kBN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  const int64_t max_tiles = ((p.R + BM - 1) / BM + p.E) * static_cast<int64_t>(p.NT);
+  const int grid = static_cast<int>(max_tiles < num_sms() ? max_tiles : num_sms());
+  fp8_gemm_kernel<kBN><<<grid, kThreads, smem, s>>>(ta, ta32, tb, p);
+  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // namespace
+
+moe_status_t launch_fp8_matmul(const moe_fp8_t& d, const uint8_t* a, const float* a_scale, const int32_t* offsets,
+                               const uint8_t* w, const float* w_scale, const uint16_t* bias, void* out, int* status,
+                               cudaStream_t s) {
+  Fp8Params p{};
+  p.R = d.R;
+  p.E = d.E;
+  p.N = d.N;
+  p.K = d.K;
+  p.KB = (d.K + 127) / 128;
+  p.NB = (d.N + 127) / 128;
+  p.out_f32 = d.out_type == MOE_T_F32;
+  p.a_scale = a_scale;
+  p.w_scale = w_scale;
+  p.offsets = offsets;
+  p.bias = bias;
+  p.out = out;
+  p.status = status;
+  // Wide tiles where there are rows for them; else narrow ones, which spread
+  // the weights over more SMs.
+  if (d.R >= 128LL * d.E) return launch<256>(p, a, w, s);
+  return launch<64>(p, a, w, s);
+}
+
+}  // namespace moe

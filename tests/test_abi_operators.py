@@ -81,3 +81,42 @@ def test_forward_few_arguments():
     assert call(**q, w1=W(w1, s1), w2=W(w2)) == 1
     assert call(**q, w1=W(None, None, w1), w2=W(w2, s2)) == 1
     assert call(**q, w1=W(w1, None, s1), w2=W(w2, s2)) == 1
+
+
+def test_fp8_sizes_and_arguments():
+    lib = moe.load()
+    D = moe.fp8_dims
+    assert moe.fp8_workspace_bytes(D(5, 3, 64, 64)) >= 4
+    for bad, code in ((D(-1, 1, 64, 64), 1), (D(4, 0, 64, 64), 1), (D(4, 1, 0, 64), 1), (D(4, 1, 64, -16), 1),
+                      (_binding.Fp8Dims(4, 1, 64, 64, 2), 1), (D(4, 257, 64, 64), 2), (D(4, 1, 72, 64), 2),
+                      (D(4, 1, 64, 72), 2), (D(4, 1, 65552, 64), 2), (D(4, 1, 64, 65552), 2)):
+        assert lib.moe_check_fp8(bad) == code
+        with pytest.raises(moe.MoeError):
+            moe.fp8_workspace_bytes(bad)
+    ar = _Arena()
+    a, sa, off, w, sw, b, out, ws = (vp(ar.take()) for _ in range(8))
+    mis = vp(ar.take() + 16)
+
+    def call(d=D(4, 3, 64, 64), a=a, sa=sa, off=off, w=w, sw=sw, b=b, out=out, ws=ws, n=256):
+        return lib.moe_fp8_matmul(d, a, sa, off, w, sw, b, out, ws, n, None)
+
+    assert call(d=D(0, 3, 64, 64), a=None, out=None) == 0  # no rows: nothing is enqueued
+    assert call(off=None) == 1  # several experts without segments
+    assert call(n=0) == 3
+    for name in ("a", "sa", "w", "sw", "out", "ws"):
+        assert call(**{name: None}) == 1 and call(**{name: mis}) == 1, name
+    assert call(off=mis) == 1 and call(b=mis) == 1
+
+
+def test_fp8_tensor_checks():
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    ok = dict(a=torch.zeros((4, 144)).to(f8), a_scale=torch.zeros((4, 2)), w=torch.zeros((2, 160, 144)).to(f8),
+              w_scale=torch.zeros((2, 2, 2)), ws=torch.zeros(256, dtype=torch.uint8),
+              offsets=torch.zeros(3, dtype=torch.int32), bias=torch.zeros((2, 160), dtype=torch.bfloat16))
+    for bad in (dict(a=torch.zeros((4, 144))), dict(a=torch.zeros((4, 160)).to(f8)), dict(a_scale=torch.zeros((4, 1))),
+                dict(w_scale=torch.zeros((2, 1, 2))), dict(offsets=None), dict(offsets=torch.zeros(3)),
+                dict(offsets=torch.zeros(2, dtype=torch.int32)), dict(bias=torch.zeros((2, 160))),
+                dict(out=torch.zeros((4, 144), dtype=f32)), dict(out=torch.zeros((4, 160), dtype=torch.float16)),
+                dict(out_dtype=torch.float16), dict(a_scale=torch.zeros((2, 4)).t())):
+        with pytest.raises(ValueError):
+            moe.fp8_matmul(**{**ok, **bad})

@@ -14,8 +14,9 @@
 // One persistent block per SM over tiles of 128 rows x kBN columns:
 //   warp 0      TMA producer: the tile's 128 x 128 block of a (a box of 32
 //               rows where the tile has no more) and kBN x 128 block of w;
-//   warp 1      allocates TMEM, issues the four K = 32 MMAs of a block;
-//   warps 2..9  eight warps, one row and half of the columns per thread: keep
+//   warp 1      allocates TMEM, issues the four K = 32 MMAs of a block (warps 2
+//               and 3 only fill the first warpgroup, which gives registers away);
+//   warps 4..11 eight warps, one row and half of the columns per thread: keep
 //               the running sums in registers and write the output.
 // Tiles are numbered expert by expert, column tile, then row tile, from the
 // offsets on the device, as in the bf16 GEMM. All waits are bounded; on a
@@ -33,7 +34,10 @@ using namespace sm100;
 constexpr int BM = 128;
 constexpr int BK = 128;               // one scale block, one 128-byte swizzle row of E4M3
 constexpr int kSmallRows = 32;        // box of a for tiles with at most this many rows
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
+// Registers per thread of the four control warps and of the eight that hold the
+// running sums: 128 x 56 + 256 x 224 is the launch's 384 x 168.
+constexpr int kRegsControl = 56, kRegsSums = 224;
 constexpr int kMaxStages = 8;
 constexpr int kABytes = BM * BK;
 constexpr uint64_t kWaitNs = 1000000000ull;
@@ -67,12 +71,30 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_
       : "memory");
 }
 
+// c0 += s * v0, c1 += s * v1 in one instruction.
+__device__ __forceinline__ void fma2(float& c0, float& c1, float s, uint32_t v0, uint32_t v1) {
+  asm("{\n\t.reg .b64 a, b, c;\n\t"
+      "mov.b64 a, {%3, %4};\n\t"
+      "mov.b64 b, {%2, %2};\n\t"
+      "mov.b64 c, {%0, %1};\n\t"
+      "fma.rn.f32x2 c, a, b, c;\n\t"
+      "mov.b64 {%0, %1}, c;\n\t}"
+      : "+f"(c0), "+f"(c1)
+      : "f"(s), "r"(v0), "r"(v1));
+}
+
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[32]) { tmem_ld_x32(taddr, v); }
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[16]) {
+  tmem_ld_x8(taddr, v);
+  tmem_ld_x8(taddr + 8, v + 8);
+}
+
 template <int kBN>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
                     const __grid_constant__ CUtensorMap tmB, const Fp8Params p) {
   constexpr int kCols = kBN / 2;             // columns per thread
-  constexpr int kLd = 16;                    // of them per TMEM load
+  constexpr int kLd = kCols < 32 ? kCols : 32;  // of them per TMEM load
   constexpr uint32_t kTmemCols = 2 * kBN < 32 ? 32 : 2 * kBN;
   constexpr uint32_t kStageBytes = kABytes + kBN * BK;
   extern __shared__ uint8_t smem_raw[];
@@ -158,8 +180,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
   const int total = tpre[p.E];
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+    if (warp == 0 && lane == 0) {
       // ---------------------------------------------------------- producer
       int stage = 0, issued = 0;
       uint32_t phase = 0;
@@ -200,9 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_wait_bounded(full_bar(stage), phase, nullptr, kWaitNs);
         }
       }
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
+    } else if (warp == 1 && lane == 0) {
       // ---------------------------------------------------------- MMA issuer
       int stage = 0, buf = 0;
       uint32_t phase = 0, buf_phase = 0;
@@ -246,9 +267,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_bounded(done_bar, 0, nullptr, kWaitNs);
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSums));
     // ------------------------------------------------- running sums and output
     const int q = warp & 3;            // TMEM lane quarter this warp may access
-    const int half = (warp - 2) / 4;   // its half of the columns
+    const int half = (warp - 4) / 4;   // its half of the columns
     int buf = 0;
     uint32_t buf_phase = 0;
     bool failed = false;
@@ -275,19 +297,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const uint32_t from = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kBN + half * kCols;
+        // the next columns' load is in flight while these are added
+        uint32_t v[2][kLd];
+        tmem_ld_cols(from, v[0]);
 #pragma unroll
         for (int c = 0; c < kCols; c += kLd) {
-          uint32_t v[kLd];
-          tmem_ld_x8(from + c, v);
-          tmem_ld_x8(from + c + 8, v + 8);
           tmem_ld_wait();
-          if (c + kLd == kCols) {
+          if (c + kLd < kCols) {
+            tmem_ld_cols(from + c + kLd, v[(c / kLd + 1) & 1]);
+          } else {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(tempty_bar(buf));
           }
 #pragma unroll
-          for (int i = 0; i < kLd; ++i) acc[c + i] = fmaf(s, __uint_as_float(v[i]), acc[c + i]);
+          for (int i = 0; i < kLd; i += 2) fma2(acc[c + i], acc[c + i + 1], s, v[(c / kLd) & 1][i], v[(c / kLd) & 1][i + 1]);
         }
         if (++buf == 2) {
           buf = 0;

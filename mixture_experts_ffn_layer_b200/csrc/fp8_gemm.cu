@@ -42,6 +42,11 @@ constexpr int kMaxStages = 8;
 constexpr int kABytes = BM * BK;
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int kCtrlBytes = 256;
+// Row scales reach the threads through shared memory, kScaleBlocks blocks of K
+// of a warp's 32 rows at a time, double-buffered (a load per thread, row and
+// block would touch 32 lines each time). Rows 9 words apart: no bank conflict.
+constexpr int kScaleBlocks = 8, kScalePitch = kScaleBlocks + 1;
+constexpr int kScaleBytes = 8 * 2 * 32 * kScalePitch * 4;
 constexpr size_t kMaxSmem = 232448;
 
 struct Fp8Params {
@@ -69,6 +74,27 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_wait_1() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+
+// mbar_wait_bounded that looks at the clock only now and then: the waits of this
+// pipeline mostly last less than a reading of it.
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+    if ((i & 63u) == 0) {
+      if (abort && *abort) return false;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitNs) return false;
+    }
+  }
+  return true;
 }
 
 // c0 += s * v0, c1 += s * v1 in one instruction.
@@ -100,7 +126,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int S = p.stages;
-  uint8_t* ctrl = smem + S * kStageBytes;
+  float* scales = reinterpret_cast<float*>(smem + S * kStageBytes);
+  uint8_t* ctrl = smem + S * kStageBytes + kScaleBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(ctrl);  // full[8] empty[8] tfull[2] tempty[2] done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * (2 * kMaxStages + 5));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -196,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t bytes = (small ? kSmallRows * BK : kABytes) + kBN * BK;
         const int brow = e * p.N + nt * kBN;
         for (int kb = 0; kb < p.KB; ++kb) {
-          if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, kWaitNs)) {
+          if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag)) {
             failed = true;
             break;
           }
@@ -220,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             stage = S - 1;
             phase ^= 1u;
           }
-          mbar_wait_bounded(full_bar(stage), phase, nullptr, kWaitNs);
+          wait_bounded(full_bar(stage), phase, nullptr);
         }
       }
     } else if (warp == 1 && lane == 0) {
@@ -233,8 +260,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         decode_tile(tile, tpre, seg, p.E, BM, e, nt, mt);
         const uint32_t idesc = idesc_e4m3_f32(BM, min(kBN, p.N - nt * kBN));
         for (int kb = 0; kb < p.KB; ++kb) {
-          if (!mbar_wait_bounded(tempty_bar(buf), buf_phase ^ 1u, abort_flag, kWaitNs) ||
-              !mbar_wait_bounded(full_bar(stage), phase, abort_flag, kWaitNs)) {
+          if (!wait_bounded(tempty_bar(buf), buf_phase ^ 1u, abort_flag) ||
+              !wait_bounded(full_bar(stage), phase, abort_flag)) {
             failed = true;
             break;
           }
@@ -264,33 +291,61 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // all MMAs issued by this thread complete before TMEM is released
       tc_commit(done_bar);
-      mbar_wait_bounded(done_bar, 0, nullptr, kWaitNs);
+      wait_bounded(done_bar, 0, nullptr);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSums));
     // ------------------------------------------------- running sums and output
     const int q = warp & 3;            // TMEM lane quarter this warp may access
     const int half = (warp - 4) / 4;   // its half of the columns
-    int buf = 0;
+    float* mine = scales + (warp - 4) * 2 * 32 * kScalePitch;
+    // Ask for the scales of blocks [kb, kb + kScaleBlocks) of the 32 rows from
+    // `first` on (past the segment's last row, that row's).
+    auto ask = [&](int first, int last, int kb, int b) {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kScaleBlocks; ++i) {
+        const int r = i * (32 / kScaleBlocks) + lane / kScaleBlocks, j = lane % kScaleBlocks;
+        if (kb + j < p.KB)
+          cp_async4(smem_u32(mine + (b * 32 + r) * kScalePitch + j),
+                    p.a_scale + static_cast<int64_t>(min(first + r, last)) * p.KB + kb + j);
+      }
+    };
+    int buf = 0, sbuf = 0;
     uint32_t buf_phase = 0;
     bool failed = false;
+    int e = 0, nt = 0, mt = 0;
+    if (blockIdx.x < total) {
+      decode_tile(blockIdx.x, tpre, seg, p.E, BM, e, nt, mt);
+      ask(seg[e] + mt * BM + q * 32, seg[e + 1] - 1, 0, 0);
+    }
+    cp_async_commit();
     for (int tile = blockIdx.x; tile < total && !failed; tile += gridDim.x) {
-      int e, nt, mt;
-      decode_tile(tile, tpre, seg, p.E, BM, e, nt, mt);
       const int row = seg[e] + mt * BM + q * 32 + lane;
       const bool valid = row < seg[e + 1];
       const int n0 = nt * kBN + half * kCols;
-      // (a row past the segment repeats its last one's scales; nothing of it is written)
-      const float* sa = p.a_scale + static_cast<int64_t>(valid ? row : seg[e + 1] - 1) * p.KB;
       const float* sw = p.w_scale + (static_cast<int64_t>(e) * p.NB + min(n0 / 128, p.NB - 1)) * p.KB;
+      const int this_e = e, first = seg[e] + mt * BM + q * 32, last = seg[e + 1] - 1;
+      if (tile + static_cast<int>(gridDim.x) < total) decode_tile(tile + gridDim.x, tpre, seg, p.E, BM, e, nt, mt);
       float acc[kCols];
 #pragma unroll
       for (int c = 0; c < kCols; ++c) acc[c] = 0.0f;
-      float s_next = __ldg(sa) * __ldg(sw);
+      float w_next = __ldg(sw);
       for (int kb = 0; kb < p.KB; ++kb) {
-        const float s = s_next;
-        if (kb + 1 < p.KB) s_next = __ldg(sa + kb + 1) * __ldg(sw + kb + 1);
-        const bool ok = mbar_wait_bounded(tfull_bar(buf), buf_phase, abort_flag, kWaitNs);
+        if (kb % kScaleBlocks == 0) {
+          // the following blocks' scales, the next tile's first after the last
+          if (kb + kScaleBlocks < p.KB)
+            ask(first, last, kb + kScaleBlocks, sbuf ^ 1);
+          else if (tile + static_cast<int>(gridDim.x) < total)
+            ask(seg[e] + mt * BM + q * 32, seg[e + 1] - 1, 0, sbuf ^ 1);
+          cp_async_commit();
+          cp_async_wait_1();
+          __syncwarp();
+          sbuf ^= 1;
+        }
+        const float s = mine[((sbuf ^ 1) * 32 + lane) * kScalePitch + kb % kScaleBlocks] * w_next;
+        if (kb + 1 < p.KB) w_next = __ldg(sw + kb + 1);
+        const bool ok = wait_bounded(tfull_bar(buf), buf_phase, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) {
           failed = true;
           break;
@@ -329,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < kCols; c += 16) {
         if (n0 + c >= p.N) break;  // (uniform; N is a multiple of 16)
         if (p.bias) {
-          const uint4* b = reinterpret_cast<const uint4*>(p.bias + static_cast<int64_t>(e) * p.N + n0 + c);
+          const uint4* b = reinterpret_cast<const uint4*>(p.bias + static_cast<int64_t>(this_e) * p.N + n0 + c);
           float f[8];
           unpack8(__ldg(b), f);
 #pragma unroll
@@ -358,6 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
+  asm volatile("cp.async.wait_all;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -387,7 +443,7 @@ moe_status_t launch(Fp8Params p, const uint8_t* a, const uint8_t* w, cudaStream_
       !make_tmap_u8(&tb, w, p.K, static_cast<uint64_t>(p.E) * p.N, kBN))
     return MOE_ERR_CUDA;
   constexpr size_t stage = kABytes + kBN * BK;
-  const size_t fixed = 1024 + kCtrlBytes + 2 * (p.E + 1) * sizeof(int);
+  const size_t fixed = 1024 + kCtrlBytes + kScaleBytes + 2 * (p.E + 1) * sizeof(int);
   p.stages = static_cast<int>((kMaxSmem - fixed) / stage);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   p.NT = (p.N + kBN - 1) / kBN;

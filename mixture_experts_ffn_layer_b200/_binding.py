@@ -113,8 +113,8 @@ def _p(t: Optional[torch.Tensor]):
 
 
 def _stream(stream=None):
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # (the raw handle: building a torch.cuda.Stream around it takes longer than a small launch)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream)
 
 

@@ -18,17 +18,37 @@ def _require(cond: bool, what: str):
         raise ValueError(what)
 
 
+def _on(device: torch.device, call, *args):
+    """call(*args) with `device` current."""
+    if device.type == "cuda" and device.index == torch.cuda.current_device():
+        return call(*args)
+    with torch.cuda.device(device):
+        return call(*args)
+
+
 def _norm_dims(x: torch.Tensor, gamma: torch.Tensor, eps: float, residual: Optional[torch.Tensor]) -> B.NormDims:
     _require(x.dim() == 2 and x.dtype == BF16 and x.stride(1) == 1, "x must be a (T, D) bf16 tensor of dense rows")
     T, D = x.shape
-    _require(gamma.shape == (D,) and gamma.dtype == BF16 and gamma.is_contiguous(), "gamma must be a (D,) bf16 tensor")
-    _require(gamma.device == x.device, "gamma and x must be on one device")
+    _require(gamma.dtype == BF16 and gamma.dim() == 1 and gamma.shape[0] == D and gamma.is_contiguous() and
+             gamma.device == x.device, "gamma must be a (D,) bf16 tensor on x's device")
+    f32 = False
     if residual is not None:
-        _require(residual.shape == x.shape and residual.dtype in (BF16, torch.float32) and residual.is_contiguous(),
-                 "residual must be a contiguous (T, D) bf16 or fp32 tensor")
-        _require(residual.device == x.device, "residual and x must be on one device")
-    f32 = residual is not None and residual.dtype == torch.float32
+        f32 = residual.dtype == torch.float32
+        _require((f32 or residual.dtype == BF16) and residual.shape == x.shape and residual.is_contiguous() and
+                 residual.device == x.device, "residual must be a contiguous (T, D) bf16 or fp32 tensor on x's device")
     return B.NormDims(T, D, x.stride(0) if T > 1 else max(D, 1), eps, B.MOE_T_F32 if f32 else B.MOE_T_BF16)
+
+
+def _like(out: Optional[torch.Tensor], of: Optional[torch.Tensor], dtype, what: str) -> Optional[torch.Tensor]:
+    """`out` checked against `of`'s shape and device, or a new tensor; None without `of`."""
+    if of is None:
+        _require(out is None, f"{what} without a residual")
+        return None
+    if out is None:
+        return of.new_empty(of.shape)
+    _require(out.shape == of.shape and out.dtype == dtype and out.is_contiguous() and out.device == of.device,
+             f"{what} must be a contiguous (T, D) tensor of its input's type, on its device")
+    return out
 
 
 def rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-5, residual: Optional[torch.Tensor] = None,
@@ -38,10 +58,9 @@ def rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-5, residual: O
     y = RMSNorm(s) * gamma in bf16. Rows of x may be strided. ``res_out`` may
     be the residual itself."""
     n = _norm_dims(x, gamma, eps, residual)
-    y = out if out is not None else torch.empty(x.shape, dtype=BF16, device=x.device)
-    res = res_out if res_out is not None or residual is None else torch.empty_like(residual)
-    with torch.cuda.device(x.device):
-        B.moe_rmsnorm(n, x, residual, gamma, res, y, None, None, stream)
+    y = _like(out, x, BF16, "out")
+    res = _like(res_out, residual, None if residual is None else residual.dtype, "res_out")
+    _on(x.device, B.moe_rmsnorm, n, x, residual, gamma, res, y, None, None, stream)
     return y, res
 
 
@@ -52,11 +71,10 @@ def rmsnorm_fp8(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-5, residua
     per row and 128 columns."""
     n = _norm_dims(x, gamma, eps, residual)
     T, D = x.shape
-    q = torch.empty((T, D), dtype=torch.float8_e4m3fn, device=x.device)
-    scale = torch.empty((T, -(-D // 128)), dtype=torch.float32, device=x.device)
-    res = res_out if res_out is not None or residual is None else torch.empty_like(residual)
-    with torch.cuda.device(x.device):
-        B.moe_rmsnorm(n, x, residual, gamma, res, None, q, scale, stream)
+    q = x.new_empty((T, D), dtype=torch.float8_e4m3fn)
+    scale = x.new_empty((T, -(-D // 128)), dtype=torch.float32)
+    res = _like(res_out, residual, None if residual is None else residual.dtype, "res_out")
+    _on(x.device, B.moe_rmsnorm, n, x, residual, gamma, res, None, q, scale, stream)
     return q, scale, res
 
 
@@ -73,20 +91,20 @@ def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale:
     E, N, _ = w.shape
     kb, nb = -(-K // 128), -(-N // 128)
     _require(a.dtype == torch.float8_e4m3fn and w.dtype == torch.float8_e4m3fn, "a and w must be float8_e4m3fn")
-    _require(a_scale.shape == (R, kb) and w_scale.shape == (E, nb, kb) and a_scale.dtype == torch.float32 and
-             w_scale.dtype == torch.float32, "a_scale must be (R, K/128) and w_scale (E, N/128, K/128) fp32")
-    _require(offsets is not None or E == 1, "E > 1 needs offsets")
-    _require(offsets is None or (offsets.shape == (E + 1,) and offsets.dtype == torch.int32),
-             "offsets must be (E+1,) int32")
+    _require(a_scale.dtype == torch.float32 and w_scale.dtype == torch.float32 and a_scale.shape == (R, kb) and
+             w_scale.shape == (E, nb, kb), "a_scale must be (R, K/128) and w_scale (E, N/128, K/128) fp32")
+    _require(E == 1 if offsets is None else offsets.shape == (E + 1,) and offsets.dtype == torch.int32,
+             "offsets must be (E+1,) int32, or None with E = 1")
     _require(bias is None or (bias.shape == (E, N) and bias.dtype == BF16), "bias must be (E, N) bf16")
     if out is None:
         _require(out_dtype in (BF16, torch.float32), "out_dtype must be bf16 or fp32")
-        out = torch.empty((R, N), dtype=out_dtype, device=a.device)
+        out = a.new_empty((R, N), dtype=out_dtype)
     _require(out.shape == (R, N) and out.dtype in (BF16, torch.float32), "out must be (R, N) bf16 or fp32")
+    device = a.device
     for t in (a, a_scale, w, w_scale, ws, offsets, bias, out):
-        _require(t is None or (t.is_contiguous() and t.device == a.device), "tensors must be contiguous and on one device")
-    with torch.cuda.device(a.device):
-        B.moe_fp8_matmul(B.fp8_dims(R, E, N, K, out.dtype), a, a_scale, offsets, w, w_scale, bias, out, ws, stream)
+        _require(t is None or (t.is_contiguous() and t.device == device), "tensors must be contiguous and on one device")
+    _on(device, B.moe_fp8_matmul, B.fp8_dims(R, E, N, K, out.dtype), a, a_scale, offsets, w, w_scale, bias, out, ws,
+        stream)
     return out
 
 

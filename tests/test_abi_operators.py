@@ -41,7 +41,8 @@ def test_rmsnorm_tensor_checks():
     x = torch.zeros((4, 64), dtype=torch.bfloat16)
     g = torch.ones(64, dtype=torch.bfloat16)
     for bad in (dict(x=x.float()), dict(x=x[0]), dict(x=x.t()), dict(gamma=g[:32]), dict(gamma=g.float()),
-                dict(residual=x[:2]), dict(residual=x.half()), dict(residual=torch.zeros((4, 128), dtype=torch.bfloat16)[:, :64])):
+                dict(residual=x[:2]), dict(residual=x.half()), dict(res_out=x), dict(out=x[:2]), dict(out=x.float()),
+                dict(residual=x, res_out=x.float()), dict(residual=torch.zeros((4, 128), dtype=torch.bfloat16)[:, :64])):
         with pytest.raises(ValueError):
             moe.rmsnorm(**{"x": x, "gamma": g, **bad})
 

@@ -12,10 +12,12 @@
 // the other of two TMEM buffers.
 //
 // One persistent block per SM over tiles of 128 rows x kBN columns:
-//   warp 0      TMA producer: the tile's 128 x 128 block of a (a box of 32
+//   warps 0, 3  TMA producers of the tile's 128 x 128 block of a (a box of 32
 //               rows where the tile has no more) and kBN x 128 block of w;
-//   warp 1      allocates TMEM, issues the four K = 32 MMAs of a block (warps 2
-//               and 3 only fill the first warpgroup, which gives registers away);
+//   warps 1, 2  issue the four K = 32 MMAs of the even and the odd blocks (the
+//               commits after every block hold an issuer up, so two take turns;
+//               each always meets the same ring slots and TMEM buffers, both
+//               even in number); warp 1 allocates TMEM;
 //   warps 4..11 eight warps, one row and half of the columns per thread: keep
 //               the running sums in registers and write the output.
 // Tiles are numbered expert by expert, column tile, then row tile, from the
@@ -39,9 +41,10 @@ constexpr int kThreads = 384;
 // running sums: 128 x 56 + 256 x 224 is the launch's 384 x 168.
 constexpr int kRegsControl = 56, kRegsSums = 224;
 constexpr int kMaxStages = 8;
+constexpr int kMaxBufs = 8;
 constexpr int kABytes = BM * BK;
 constexpr uint64_t kWaitNs = 1000000000ull;
-constexpr int kCtrlBytes = 256;
+constexpr int kCtrlBytes = 512;
 // Row scales reach the threads through shared memory, kScaleBlocks blocks of K
 // of a warp's 32 rows at a time, double-buffered (a load per thread, row and
 // block would touch 32 lines each time). Rows 9 words apart: no bank conflict.
@@ -66,12 +69,15 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate) {
+// D[tmem] (+)= A * B^T over K = 32, by a whole warp with one lane elected to
+// issue (the operands stay warp-uniform, which keeps the issue short).
+__device__ __forceinline__ void mma_f8_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "{\n\t.reg .pred e, q;\n\t.reg .b32 r;\n\t"
+      "setp.ne.b32 q, %4, 0;\n\t"
+      "elect.sync r|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, q;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
@@ -121,27 +127,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap tmB, const Fp8Params p) {
   constexpr int kCols = kBN / 2;             // columns per thread
   constexpr int kLd = kCols < 32 ? kCols : 32;  // of them per TMEM load
-  constexpr uint32_t kTmemCols = 2 * kBN < 32 ? 32 : 2 * kBN;
+  constexpr int kBufs = kMaxBufs * kBN <= 512 ? kMaxBufs : 512 / kBN;  // TMEM buffers
+  constexpr uint32_t kTmemCols = kBufs * kBN;  // a power of two
   constexpr uint32_t kStageBytes = kABytes + kBN * BK;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int S = p.stages;
   float* scales = reinterpret_cast<float*>(smem + S * kStageBytes);
   uint8_t* ctrl = smem + S * kStageBytes + kScaleBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ctrl);  // full[8] empty[8] tfull[2] tempty[2] done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * (2 * kMaxStages + 5));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ctrl);  // full[8] empty[8] tfull[8] tempty[8] done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * (2 * kMaxStages + 2 * kMaxBufs + 1));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* bad_s = reinterpret_cast<int*>(tmem_slot + 2);
   int* seg = reinterpret_cast<int*>(ctrl + kCtrlBytes);  // E+1 segment starts
   int* tpre = seg + (p.E + 1);                           // E+1 tile prefix
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0), lane = threadIdx.x % 32;
   const uint32_t bar0 = smem_u32(bars);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
   auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * kMaxStages + b); };
-  auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * kMaxStages + 2 + b); };
-  const uint32_t done_bar = bar0 + 8u * (2 * kMaxStages + 4);
+  auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * kMaxStages + kMaxBufs + b); };
+  const uint32_t done_bar = bar0 + 8u * (2 * kMaxStages + 2 * kMaxBufs);
 
   // ---- prologue: segment table, tile prefix, barriers, TMEM
   if (threadIdx.x == 0) {
@@ -184,14 +191,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         tpre[p.E] = 0;
       }
       for (int s = 0; s < S; ++s) {
-        mbar_init(full_bar(s), 1);
+        mbar_init(full_bar(s), 2);  // both producers
         mbar_init(empty_bar(s), 1);
       }
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < kBufs; ++b) {
         mbar_init(tfull_bar(b), 1);
         mbar_init(tempty_bar(b), 8);
       }
-      mbar_init(done_bar, 1);
+      mbar_init(done_bar, 2);
       fence_mbar_init();
       tma_prefetch_desc(&tmA);
       tma_prefetch_desc(&tmA32);
@@ -209,88 +216,92 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
-    if (warp == 0 && lane == 0) {
-      // ---------------------------------------------------------- producer
-      int stage = 0, issued = 0;
-      uint32_t phase = 0;
-      bool failed = false;
-      for (int tile = blockIdx.x; tile < total && !failed; tile += gridDim.x) {
-        int e, nt, mt;
-        decode_tile(tile, tpre, seg, p.E, BM, e, nt, mt);
-        const int row0 = seg[e] + mt * BM;
-        const bool small = seg[e + 1] - row0 <= kSmallRows;
-        const CUtensorMap* ta = small ? &tmA32 : &tmA;
-        const uint32_t bytes = (small ? kSmallRows * BK : kABytes) + kBN * BK;
-        const int brow = e * p.N + nt * kBN;
-        for (int kb = 0; kb < p.KB; ++kb) {
-          if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag)) {
-            failed = true;
-            break;
+    if (warp == 0 || warp == 3) {
+      if (lane == 0) {
+        // -------------------------------------------------------- producers
+        int stage = 0, issued = 0;
+        uint32_t phase = 0;
+        bool failed = false;
+        for (int tile = blockIdx.x; tile < total && !failed; tile += gridDim.x) {
+          int e, nt, mt;
+          decode_tile(tile, tpre, seg, p.E, BM, e, nt, mt);
+          const int row0 = seg[e] + mt * BM;
+          const bool small = seg[e + 1] - row0 <= kSmallRows;
+          const CUtensorMap* map = warp == 3 ? &tmB : small ? &tmA32 : &tmA;
+          const uint32_t bytes = warp == 3 ? kBN * BK : small ? kSmallRows * BK : kABytes;
+          const int at = warp == 3 ? e * p.N + nt * kBN : row0;
+          for (int kb = 0; kb < p.KB; ++kb) {
+            if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag)) {
+              failed = true;
+              break;
+            }
+            mbar_arrive_expect_tx(full_bar(stage), bytes);
+            tma_load_2d(smem_u32(smem + stage * kStageBytes) + (warp == 3 ? kABytes : 0), map, full_bar(stage), kb * BK, at);
+            ++issued;
+            if (++stage == S) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
-          const uint32_t a_dst = smem_u32(smem + stage * kStageBytes);
-          mbar_arrive_expect_tx(full_bar(stage), bytes);
-          tma_load_2d(a_dst + kABytes, &tmB, full_bar(stage), kb * BK, brow);
-          tma_load_2d(a_dst, ta, full_bar(stage), kb * BK, row0);
-          ++issued;
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
+        }
+        if (failed) {
+          record_status(p.status, MOE_ERR_TIMEOUT);
+          *abort_flag = 1;
+          // let the copies still in flight land before the CTA can exit
+          for (int i = issued < S ? issued : S; i > 0; --i) {
+            if (--stage < 0) {
+              stage = S - 1;
+              phase ^= 1u;
+            }
+            wait_bounded(full_bar(stage), phase, nullptr);
           }
         }
       }
-      if (failed) {
-        record_status(p.status, MOE_ERR_TIMEOUT);
-        *abort_flag = 1;
-        // let the copies still in flight land before the CTA can exit
-        for (int i = issued < S ? issued : S; i > 0; --i) {
-          if (--stage < 0) {
-            stage = S - 1;
-            phase ^= 1u;
-          }
-          wait_bounded(full_bar(stage), phase, nullptr);
-        }
-      }
-    } else if (warp == 1 && lane == 0) {
-      // ---------------------------------------------------------- MMA issuer
+    } else {
+      // ---------------------------------------------------------- MMA issuers
+      const int mine = warp - 1;  // parity of this issuer's blocks, counted over all tiles
       int stage = 0, buf = 0;
-      uint32_t phase = 0, buf_phase = 0;
+      uint32_t phase = 0, buf_phase = 0, count = 0;
       bool failed = false;
       for (int tile = blockIdx.x; tile < total && !failed; tile += gridDim.x) {
         int e, nt, mt;
         decode_tile(tile, tpre, seg, p.E, BM, e, nt, mt);
         const uint32_t idesc = idesc_e4m3_f32(BM, min(kBN, p.N - nt * kBN));
-        for (int kb = 0; kb < p.KB; ++kb) {
-          if (!wait_bounded(tempty_bar(buf), buf_phase ^ 1u, abort_flag) ||
-              !wait_bounded(full_bar(stage), phase, abort_flag)) {
-            failed = true;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t d_tmem = tmem_base + buf * kBN;
-          const uint32_t a_addr = smem_u32(smem + stage * kStageBytes);
-          const uint32_t b_addr = a_addr + kABytes;
+        for (int kb = 0; kb < p.KB; ++kb, ++count) {
+          if (static_cast<int>(count & 1u) == mine) {
+            if (!__all_sync(0xffffffffu, wait_bounded(tempty_bar(buf), buf_phase ^ 1u, abort_flag) &&
+                                             wait_bounded(full_bar(stage), phase, abort_flag))) {
+              failed = true;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t d_tmem = tmem_base + buf * kBN;
+            const uint32_t a_addr = smem_u32(smem + stage * kStageBytes);
+            const uint32_t b_addr = a_addr + kABytes;
 #pragma unroll
-          for (int kk = 0; kk < BK / 32; ++kk)
-            mma_f8(d_tmem, desc_kmajor_sw128(a_addr + kk * 32), desc_kmajor_sw128(b_addr + kk * 32), idesc,
-                   kk != 0 ? 1u : 0u);
-          tc_commit(empty_bar(stage));
-          tc_commit(tfull_bar(buf));
+            for (int kk = 0; kk < BK / 32; ++kk)
+              mma_f8_elect(d_tmem, desc_kmajor_sw128(a_addr + kk * 32), desc_kmajor_sw128(b_addr + kk * 32), idesc,
+                           kk != 0 ? 1u : 0u);
+            tc_commit_elect(empty_bar(stage));
+            tc_commit_elect(tfull_bar(buf));
+          }
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
           }
-          if (++buf == 2) {
+          if (++buf == kBufs) {
             buf = 0;
             buf_phase ^= 1u;
           }
         }
       }
-      if (failed) {
+      if (failed && lane == 0) {
         record_status(p.status, MOE_ERR_TIMEOUT);
         *abort_flag = 1;
       }
-      // all MMAs issued by this thread complete before TMEM is released
-      tc_commit(done_bar);
+      // all MMAs issued by this warp complete before TMEM is released
+      __syncwarp();
+      tc_commit_elect(done_bar);
       wait_bounded(done_bar, 0, nullptr);
     }
   } else {
@@ -368,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < kLd; i += 2) fma2(acc[c + i], acc[c + i + 1], s, v[(c / kLd) & 1][i], v[(c / kLd) & 1][i + 1]);
         }
-        if (++buf == 2) {
+        if (++buf == kBufs) {
           buf = 0;
           buf_phase ^= 1u;
         }
@@ -445,7 +456,7 @@ moe_status_t launch(Fp8Params p, const uint8_t* a, const uint8_t* w, cudaStream_
   constexpr size_t stage = kABytes + kBN * BK;
   const size_t fixed = 1024 + kCtrlBytes + kScaleBytes + 2 * (p.E + 1) * sizeof(int);
   p.stages = static_cast<int>((kMaxSmem - fixed) / stage);
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  p.stages = p.stages > kMaxStages ? kMaxStages : p.stages / 2 * 2;
   p.NT = (p.N + kBN - 1) / kBN;
   const size_t smem = fixed + p.stages * stage;
   if (cudaFuncSetAttribute(fp8_gemm_kernel<kBN>, cudaFuncAttributeMaxDynamicSharedMemorySize,

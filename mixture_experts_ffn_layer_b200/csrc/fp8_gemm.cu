@@ -23,6 +23,8 @@
 // Tiles are numbered expert by expert, column tile, then row tile, from the
 // offsets on the device, as in the bf16 GEMM. All waits are bounded; on a
 // timeout the kernel records it, drains what is in flight and returns.
+#include <algorithm>
+
 #include "common.cuh"
 #include "gemm_common.cuh"
 #include "sm100.cuh"
@@ -36,20 +38,17 @@ using namespace sm100;
 constexpr int BM = 128;
 constexpr int BK = 128;               // one scale block, one 128-byte swizzle row of E4M3
 constexpr int kSmallRows = 32;        // box of a for tiles with at most this many rows
-constexpr int kThreads = 384;
-// Registers per thread of the four control warps and of the eight that hold the
-// running sums: 128 x 56 + 256 x 224 is the launch's 384 x 168.
-constexpr int kRegsControl = 56, kRegsSums = 224;
 constexpr int kMaxStages = 8;
 constexpr int kMaxBufs = 8;
 constexpr int kABytes = BM * BK;
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int kCtrlBytes = 512;
-// Row scales reach the threads through shared memory, kScaleBlocks blocks of K
-// of a warp's 32 rows at a time, double-buffered (a load per thread, row and
-// block would touch 32 lines each time). Rows 9 words apart: no bank conflict.
-constexpr int kScaleBlocks = 8, kScalePitch = kScaleBlocks + 1;
-constexpr int kScaleBytes = 8 * 2 * 32 * kScalePitch * 4;
+// The scales reach the threads through shared memory, kScaleBlocks blocks of K
+// of a warp's 32 rows and of its columns at a time, double-buffered (a load per
+// thread and block would touch 32 lines each time, and be waited for). Rows 9
+// words apart: no bank conflict.
+constexpr int kScaleBlocks = 8, kScalePitch = kScaleBlocks + 1, kScaleRows = 33;
+constexpr int kScaleBytes = 2 * kScaleRows * kScalePitch * 4;  // per warp
 constexpr size_t kMaxSmem = 232448;
 
 struct Fp8Params {
@@ -121,20 +120,39 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[16]) 
   tmem_ld_x8(taddr + 8, v + 8);
 }
 
-template <int kBN>
-__global__ void __launch_bounds__(kThreads, 1)
+// A tile's columns and the warps that hold its sums, and what follows.
+template <int kBN_, int kSumWarps_>
+struct Shape {
+  static constexpr int kBN = kBN_, kSumWarps = kSumWarps_;
+  static constexpr int kThreads = 128 + 32 * kSumWarps;
+  static constexpr int kCols = kBN / (kSumWarps / 4);  // columns per thread
+  // Blocks of K added at a time: a narrow tile's block is little work beside the
+  // latency of its hand-over.
+  static constexpr int kU = kCols >= 64 ? 1 : 64 / kCols;
+  static constexpr int kBufs = kMaxBufs * kBN <= 512 ? kMaxBufs : 512 / kBN / 2 * 2;  // TMEM buffers, even
+  static constexpr uint32_t kTmemCols = kBufs * kBN <= 256 ? 256 : 512;
+  static constexpr uint32_t kStageBytes = kABytes + kBN * BK;
+  // Registers per thread of the four control warps and of the others, out of
+  // what the launch gets (a multiple of 8 per thread).
+  static constexpr int kRegsLaunch = 65536 / kThreads / 8 * 8;
+  static constexpr int kRegsControl = 56;
+  static constexpr int kRegsSums = (kRegsLaunch * kThreads - 128 * kRegsControl) / (32 * kSumWarps) / 8 * 8;
+  static_assert(kRegsSums <= 255 + 1 && kCols % 16 == 0 && 128 % kCols == 0, "");
+};
+
+template <class S_>
+__global__ void __launch_bounds__(S_::kThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
                     const __grid_constant__ CUtensorMap tmB, const Fp8Params p) {
-  constexpr int kCols = kBN / 2;             // columns per thread
-  constexpr int kLd = kCols < 32 ? kCols : 32;  // of them per TMEM load
-  constexpr int kBufs = kMaxBufs * kBN <= 512 ? kMaxBufs : 512 / kBN;  // TMEM buffers
-  constexpr uint32_t kTmemCols = kBufs * kBN;  // a power of two
-  constexpr uint32_t kStageBytes = kABytes + kBN * BK;
+  constexpr int kBN = S_::kBN, kCols = S_::kCols, kU = S_::kU, kBufs = S_::kBufs, kSumWarps = S_::kSumWarps;
+  constexpr uint32_t kTmemCols = S_::kTmemCols, kStageBytes = S_::kStageBytes;
+  constexpr int kRegsControl = S_::kRegsControl, kRegsSums = S_::kRegsSums;
+  constexpr int kLd = kCols < 32 ? kCols : 32;  // columns per TMEM load
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int S = p.stages;
   float* scales = reinterpret_cast<float*>(smem + S * kStageBytes);
-  uint8_t* ctrl = smem + S * kStageBytes + kScaleBytes;
+  uint8_t* ctrl = smem + S * kStageBytes + kSumWarps * kScaleBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(ctrl);  // full[8] empty[8] tfull[8] tempty[8] done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ctrl + 8 * (2 * kMaxStages + 2 * kMaxBufs + 1));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -196,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int b = 0; b < kBufs; ++b) {
         mbar_init(tfull_bar(b), 1);
-        mbar_init(tempty_bar(b), 8);
+        mbar_init(tempty_bar(b), kSumWarps);
       }
       mbar_init(done_bar, 2);
       fence_mbar_init();
@@ -308,19 +326,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSums));
     // ------------------------------------------------- running sums and output
     const int q = warp & 3;            // TMEM lane quarter this warp may access
-    const int half = (warp - 4) / 4;   // its half of the columns
-    float* mine = scales + (warp - 4) * 2 * 32 * kScalePitch;
-    // Ask for the scales of blocks [kb, kb + kScaleBlocks) of the 32 rows from
-    // `first` on (past the segment's last row, that row's).
-    auto ask = [&](int first, int last, int kb, int b) {
+    const int part = (warp - 4) / 4;   // its part of the columns
+    float* mine = scales + (warp - 4) * 2 * kScaleRows * kScalePitch;
+    // Ask for the scales of blocks [kb, kb + kScaleBlocks) of the tile (e, nt,
+    // mt)'s 32 rows (past the segment's last row, that row's) and columns.
+    auto ask = [&](int e, int nt, int mt, int kb, int b) {
       __syncwarp();
+      const int first = seg[e] + mt * BM + q * 32, last = seg[e + 1] - 1;
+      const int j = lane % kScaleBlocks;
+      float* to = mine + b * kScaleRows * kScalePitch + j;
+      if (kb + j < p.KB) {
 #pragma unroll
-      for (int i = 0; i < kScaleBlocks; ++i) {
-        const int r = i * (32 / kScaleBlocks) + lane / kScaleBlocks, j = lane % kScaleBlocks;
-        if (kb + j < p.KB)
-          cp_async4(smem_u32(mine + (b * 32 + r) * kScalePitch + j),
-                    p.a_scale + static_cast<int64_t>(min(first + r, last)) * p.KB + kb + j);
+        for (int i = 0; i < kScaleBlocks; ++i) {
+          const int r = i * (32 / kScaleBlocks) + lane / kScaleBlocks;
+          cp_async4(smem_u32(to + r * kScalePitch), p.a_scale + static_cast<int64_t>(min(first + r, last)) * p.KB + kb + j);
+        }
+        if (lane < kScaleBlocks) {
+          const int nb = min((nt * kBN + part * kCols) / 128, p.NB - 1);
+          cp_async4(smem_u32(to + 32 * kScalePitch), p.w_scale + (static_cast<int64_t>(e) * p.NB + nb) * p.KB + kb + j);
+        }
       }
+      cp_async_commit();
     };
     int buf = 0, sbuf = 0;
     uint32_t buf_phase = 0;
@@ -328,60 +354,98 @@ __global__ void __launch_bounds__(kThreads, 1)
     int e = 0, nt = 0, mt = 0;
     if (blockIdx.x < total) {
       decode_tile(blockIdx.x, tpre, seg, p.E, BM, e, nt, mt);
-      ask(seg[e] + mt * BM + q * 32, seg[e + 1] - 1, 0, 0);
+      ask(e, nt, mt, 0, 0);
     }
-    cp_async_commit();
     for (int tile = blockIdx.x; tile < total && !failed; tile += gridDim.x) {
       const int row = seg[e] + mt * BM + q * 32 + lane;
       const bool valid = row < seg[e + 1];
-      const int n0 = nt * kBN + half * kCols;
-      const float* sw = p.w_scale + (static_cast<int64_t>(e) * p.NB + min(n0 / 128, p.NB - 1)) * p.KB;
-      const int this_e = e, first = seg[e] + mt * BM + q * 32, last = seg[e + 1] - 1;
+      const int n0 = nt * kBN + part * kCols;
+      const int this_e = e, this_nt = nt, this_mt = mt;
       if (tile + static_cast<int>(gridDim.x) < total) decode_tile(tile + gridDim.x, tpre, seg, p.E, BM, e, nt, mt);
+      // the sums start at the bias, which arrives while the first block is multiplied
       float acc[kCols];
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) acc[c] = 0.0f;
-      float w_next = __ldg(sw);
-      for (int kb = 0; kb < p.KB; ++kb) {
-        if (kb % kScaleBlocks == 0) {
+      for (int c = 0; c < kCols; c += 8) {
+        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (p.bias && n0 + c < p.N)  // (N is a multiple of 16)
+          unpack8(__ldg(reinterpret_cast<const uint4*>(p.bias + static_cast<int64_t>(this_e) * p.N + n0 + c)), f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[c + i] = f[i];
+      }
+      for (int kb0 = 0; kb0 < p.KB; kb0 += kU) {
+        if (kb0 % kScaleBlocks == 0) {
           // the following blocks' scales, the next tile's first after the last
-          if (kb + kScaleBlocks < p.KB)
-            ask(first, last, kb + kScaleBlocks, sbuf ^ 1);
+          if (kb0 + kScaleBlocks < p.KB)
+            ask(this_e, this_nt, this_mt, kb0 + kScaleBlocks, sbuf ^ 1);
           else if (tile + static_cast<int>(gridDim.x) < total)
-            ask(seg[e] + mt * BM + q * 32, seg[e + 1] - 1, 0, sbuf ^ 1);
-          cp_async_commit();
+            ask(e, nt, mt, 0, sbuf ^ 1);
+          else
+            cp_async_commit();
           cp_async_wait_1();
           __syncwarp();
           sbuf ^= 1;
         }
-        const float s = mine[((sbuf ^ 1) * 32 + lane) * kScalePitch + kb % kScaleBlocks] * w_next;
-        if (kb + 1 < p.KB) w_next = __ldg(sw + kb + 1);
-        const bool ok = wait_bounded(tfull_bar(buf), buf_phase, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) {
-          failed = true;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t from = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kBN + half * kCols;
-        // the next columns' load is in flight while these are added
-        uint32_t v[2][kLd];
-        tmem_ld_cols(from, v[0]);
+        const int n = min(kU, p.KB - kb0);
+        float s[kU];
+        const float* at = mine + (sbuf ^ 1) * kScaleRows * kScalePitch + kb0 % kScaleBlocks;
 #pragma unroll
-        for (int c = 0; c < kCols; c += kLd) {
-          tmem_ld_wait();
-          if (c + kLd < kCols) {
-            tmem_ld_cols(from + c + kLd, v[(c / kLd + 1) & 1]);
-          } else {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(tempty_bar(buf));
+        for (int u = 0; u < kU; ++u) s[u] = at[lane * kScalePitch + u] * at[32 * kScalePitch + u];
+        const uint32_t from = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + part * kCols;
+        if constexpr (kCols > 64) {
+          if (!__all_sync(0xffffffffu, wait_bounded(tfull_bar(buf), buf_phase, abort_flag))) {
+            failed = true;
+            break;
           }
+          tc_fence_after();
+          // the next columns' load is in flight while these are added
+          uint32_t v[2][kLd];
+          tmem_ld_cols(from + buf * kBN, v[0]);
 #pragma unroll
-          for (int i = 0; i < kLd; i += 2) fma2(acc[c + i], acc[c + i + 1], s, v[(c / kLd) & 1][i], v[(c / kLd) & 1][i + 1]);
-        }
-        if (++buf == kBufs) {
-          buf = 0;
-          buf_phase ^= 1u;
+          for (int c = 0; c < kCols; c += kLd) {
+            tmem_ld_wait();
+            if (c + kLd < kCols) {
+              tmem_ld_cols(from + buf * kBN + c + kLd, v[(c / kLd + 1) & 1]);
+            } else {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(tempty_bar(buf));
+            }
+#pragma unroll
+            for (int i = 0; i < kLd; i += 2)
+              fma2(acc[c + i], acc[c + i + 1], s[0], v[(c / kLd) & 1][i], v[(c / kLd) & 1][i + 1]);
+          }
+          if (++buf == kBufs) {
+            buf = 0;
+            buf_phase ^= 1u;
+          }
+        } else {
+          // kU blocks' sums out of TMEM at once: one wait for their loads
+          uint32_t v[kU][kCols];
+          const int buf0 = buf;
+#pragma unroll
+          for (int u = 0; u < kU; ++u) {
+            if (u < n) {
+              if (!__all_sync(0xffffffffu, wait_bounded(tfull_bar(buf), buf_phase, abort_flag))) failed = true;
+              tc_fence_after();
+#pragma unroll
+              for (int c = 0; c < kCols; c += kLd)
+                tmem_ld_cols(from + buf * kBN + c, *reinterpret_cast<uint32_t(*)[kLd]>(&v[u][c]));
+              if (++buf == kBufs) {
+                buf = 0;
+                buf_phase ^= 1u;
+              }
+            }
+          }
+          tmem_ld_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane < n) mbar_arrive(tempty_bar((buf0 + lane) % kBufs));
+          if (failed) break;
+#pragma unroll
+          for (int u = 0; u < kU; ++u)
+            if (u < n)
+#pragma unroll
+              for (int c = 0; c < kCols; c += 2) fma2(acc[c], acc[c + 1], s[u], v[u][c], v[u][c + 1]);
         }
       }
       if (failed) {
@@ -394,16 +458,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int c = 0; c < kCols; c += 16) {
         if (n0 + c >= p.N) break;  // (uniform; N is a multiple of 16)
-        if (p.bias) {
-          const uint4* b = reinterpret_cast<const uint4*>(p.bias + static_cast<int64_t>(this_e) * p.N + n0 + c);
-          float f[8];
-          unpack8(__ldg(b), f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) acc[c + i] += f[i];
-          unpack8(__ldg(b + 1), f);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) acc[c + 8 + i] += f[i];
-        }
         if (!valid) continue;
         const int64_t at = static_cast<int64_t>(row) * p.N + n0 + c;
         if (p.out_f32) {
@@ -447,24 +501,24 @@ bool make_tmap_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t r
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kBN>
+template <class S_>
 moe_status_t launch(Fp8Params p, const uint8_t* a, const uint8_t* w, cudaStream_t s) {
   CUtensorMap ta, ta32, tb;
   if (!make_tmap_u8(&ta, a, p.K, p.R, BM) || !make_tmap_u8(&ta32, a, p.K, p.R, kSmallRows) ||
-      !make_tmap_u8(&tb, w, p.K, static_cast<uint64_t>(p.E) * p.N, kBN))
+      !make_tmap_u8(&tb, w, p.K, static_cast<uint64_t>(p.E) * p.N, S_::kBN))
     return MOE_ERR_CUDA;
-  constexpr size_t stage = kABytes + kBN * BK;
-  const size_t fixed = 1024 + kCtrlBytes + kScaleBytes + 2 * (p.E + 1) * sizeof(int);
+  constexpr size_t stage = S_::kStageBytes;
+  const size_t fixed = 1024 + kCtrlBytes + S_::kSumWarps * kScaleBytes + 2 * (p.E + 1) * sizeof(int);
   p.stages = static_cast<int>((kMaxSmem - fixed) / stage);
   p.stages = p.stages > kMaxStages ? kMaxStages : p.stages / 2 * 2;
-  p.NT = (p.N + kBN - 1) / kBN;
+  p.NT = (p.N + S_::kBN - 1) / S_::kBN;
   const size_t smem = fixed + p.stages * stage;
-  if (cudaFuncSetAttribute(fp8_gemm_kernel<kBN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(fp8_gemm_kernel<S_>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem)) != cudaSuccess)
     return MOE_ERR_CUDA;
   const int64_t max_tiles = ((p.R + BM - 1) / BM + p.E) * static_cast<int64_t>(p.NT);
   const int grid = static_cast<int>(max_tiles < num_sms() ? max_tiles : num_sms());
-  fp8_gemm_kernel<kBN><<<grid, kThreads, smem, s>>>(ta, ta32, tb, p);
+  fp8_gemm_kernel<S_><<<grid, S_::kThreads, smem, s>>>(ta, ta32, tb, p);
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -487,10 +541,24 @@ moe_status_t launch_fp8_matmul(const moe_fp8_t& d, const uint8_t* a, const float
   p.bias = bias;
   p.out = out;
   p.status = status;
-  // Wide tiles where there are rows for them; else narrow ones, which spread
-  // the weights over more SMs.
-  if (d.R >= 128LL * d.E) return launch<256>(p, a, w, s);
-  return launch<64>(p, a, w, s);
+  // The tile whose rounds over the SMs cost least: a block of K takes 0.68 us at
+  // 256 columns (0.82 where tiles have few rows and the weights' stream sets the
+  // time), 0.64 at 192, 0.36 at 64 (measured at 8192 x 5760 and on 9 rows an
+  // expert); rounds are estimated from the row tiles, half a round for the tail.
+  // So long batches take 256 columns (8192 x 5760 x 2880: 155 us against 191 at
+  // 192), decode batches of many experts 192 (256 rows on 32 experts of 2880 x
+  // 2880: 51 us against 66 at 128 and 78 at 64), single decode projections 64
+  // (17 x 5760 x 2880: 14.8 us against 18.4 at 192).
+  const bool few = d.R < 64LL * d.E;
+  const int64_t mtiles = few ? std::min(d.E, d.R) : d.R / 128 + d.E;
+  auto cost = [&](int bn, double us) {
+    const double rounds = static_cast<double>(mtiles * ((d.N + bn - 1) / bn)) / num_sms() + 0.5;
+    return us * (rounds < 1.0 ? 1.0 : rounds);
+  };
+  const double c256 = cost(256, few ? 0.82 : 0.68), c192 = cost(192, 0.64), c64 = cost(64, 0.36);
+  if (c64 <= c192 && c64 <= c256) return launch<Shape<64, 8>>(p, a, w, s);
+  if (c192 <= c256) return launch<Shape<192, 12>>(p, a, w, s);
+  return launch<Shape<256, 8>>(p, a, w, s);
 }
 
 }  // namespace moe

@@ -114,11 +114,28 @@ __device__ __forceinline__ void fma2(float& c0, float& c1, float s, uint32_t v0,
       : "f"(s), "r"(v0), "r"(v1));
 }
 
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[32]) { tmem_ld_x32(taddr, v); }
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[16]) {
-  tmem_ld_x8(taddr, v);
-  tmem_ld_x8(taddr + 8, v + 8);
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
+        "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]),
+        "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]),
+        "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+        "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]),
+        "=r"(v[30]), "=r"(v[31]), "=r"(v[32]), "=r"(v[33]), "=r"(v[34]), "=r"(v[35]),
+        "=r"(v[36]), "=r"(v[37]), "=r"(v[38]), "=r"(v[39]), "=r"(v[40]), "=r"(v[41]),
+        "=r"(v[42]), "=r"(v[43]), "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]),
+        "=r"(v[48]), "=r"(v[49]), "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]),
+        "=r"(v[54]), "=r"(v[55]), "=r"(v[56]), "=r"(v[57]), "=r"(v[58]), "=r"(v[59]),
+        "=r"(v[60]), "=r"(v[61]), "=r"(v[62]), "=r"(v[63])
+      : "r"(taddr)
+      : "memory");
 }
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[32]) { tmem_ld_x32(taddr, v); }
 
 // A tile's columns and the warps that hold its sums, and what follows.
 template <int kBN_, int kSumWarps_>
@@ -147,7 +164,7 @@ __global__ void __launch_bounds__(S_::kThreads, 1)
   constexpr int kBN = S_::kBN, kCols = S_::kCols, kU = S_::kU, kBufs = S_::kBufs, kSumWarps = S_::kSumWarps;
   constexpr uint32_t kTmemCols = S_::kTmemCols, kStageBytes = S_::kStageBytes;
   constexpr int kRegsControl = S_::kRegsControl, kRegsSums = S_::kRegsSums;
-  constexpr int kLd = kCols < 32 ? kCols : 32;  // columns per TMEM load
+  constexpr int kLd = kCols < 64 ? kCols : 64;  // columns per TMEM load
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int S = p.stages;
@@ -397,22 +414,19 @@ __global__ void __launch_bounds__(S_::kThreads, 1)
             break;
           }
           tc_fence_after();
-          // the next columns' load is in flight while these are added
-          uint32_t v[2][kLd];
-          tmem_ld_cols(from + buf * kBN, v[0]);
+          // half of the columns at a time
+          uint32_t v[kLd];
 #pragma unroll
           for (int c = 0; c < kCols; c += kLd) {
+            tmem_ld_cols(from + buf * kBN + c, v);
             tmem_ld_wait();
-            if (c + kLd < kCols) {
-              tmem_ld_cols(from + buf * kBN + c + kLd, v[(c / kLd + 1) & 1]);
-            } else {
+            if (c + kLd == kCols) {
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(tempty_bar(buf));
             }
 #pragma unroll
-            for (int i = 0; i < kLd; i += 2)
-              fma2(acc[c + i], acc[c + i + 1], s[0], v[(c / kLd) & 1][i], v[(c / kLd) & 1][i + 1]);
+            for (int i = 0; i < kLd; i += 2) fma2(acc[c + i], acc[c + i + 1], s[0], v[i], v[i + 1]);
           }
           if (++buf == kBufs) {
             buf = 0;

@@ -114,7 +114,8 @@ __device__ __forceinline__ void fma2(float& c0, float& c1, float s, uint32_t v0,
       : "f"(s), "r"(v0), "r"(v1));
 }
 
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[64]) {
+// 32 lanes x 64 consecutive 32-bit columns per thread.
+__device__ __forceinline__ void tmem_ld_x64(uint32_t taddr, uint32_t (&v)[64]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
       "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -135,36 +136,33 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[64]) 
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[32]) { tmem_ld_x32(taddr, v); }
-
 // A tile's columns and the warps that hold its sums, and what follows.
 template <int kBN_, int kSumWarps_>
 struct Shape {
   static constexpr int kBN = kBN_, kSumWarps = kSumWarps_;
   static constexpr int kThreads = 128 + 32 * kSumWarps;
   static constexpr int kCols = kBN / (kSumWarps / 4);  // columns per thread
-  // Blocks of K added at a time: a narrow tile's block is little work beside the
-  // latency of its hand-over.
-  static constexpr int kU = kCols >= 64 ? 1 : 64 / kCols;
   static constexpr int kBufs = kMaxBufs * kBN <= 512 ? kMaxBufs : 512 / kBN / 2 * 2;  // TMEM buffers, even
   static constexpr uint32_t kTmemCols = kBufs * kBN <= 256 ? 256 : 512;
   static constexpr uint32_t kStageBytes = kABytes + kBN * BK;
   // Registers per thread of the four control warps and of the others, out of
-  // what the launch gets (a multiple of 8 per thread).
+  // what the launch gets (a multiple of 8 per thread); four warps of sums have
+  // enough as it is.
+  static constexpr bool kMoveRegs = kSumWarps > 4;
   static constexpr int kRegsLaunch = 65536 / kThreads / 8 * 8;
   static constexpr int kRegsControl = 56;
   static constexpr int kRegsSums = (kRegsLaunch * kThreads - 128 * kRegsControl) / (32 * kSumWarps) / 8 * 8;
-  static_assert(kRegsSums <= 255 + 1 && kCols % 16 == 0 && 128 % kCols == 0, "");
+  static_assert(!kMoveRegs || (kRegsSums > kRegsLaunch && kRegsSums <= 232), "");
+  static_assert(kCols % 64 == 0 && 128 % kCols == 0, "");
 };
 
 template <class S_>
 __global__ void __launch_bounds__(S_::kThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
                     const __grid_constant__ CUtensorMap tmB, const Fp8Params p) {
-  constexpr int kBN = S_::kBN, kCols = S_::kCols, kU = S_::kU, kBufs = S_::kBufs, kSumWarps = S_::kSumWarps;
+  constexpr int kBN = S_::kBN, kCols = S_::kCols, kBufs = S_::kBufs, kSumWarps = S_::kSumWarps;
   constexpr uint32_t kTmemCols = S_::kTmemCols, kStageBytes = S_::kStageBytes;
   constexpr int kRegsControl = S_::kRegsControl, kRegsSums = S_::kRegsSums;
-  constexpr int kLd = kCols < 64 ? kCols : 64;  // columns per TMEM load
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int S = p.stages;
@@ -250,7 +248,7 @@ __global__ void __launch_bounds__(S_::kThreads, 1)
   const int total = tpre[p.E];
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+    if constexpr (S_::kMoveRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
     if (warp == 0 || warp == 3) {
       if (lane == 0) {
         // -------------------------------------------------------- producers
@@ -340,45 +338,57 @@ __global__ void __launch_bounds__(S_::kThreads, 1)
       wait_bounded(done_bar, 0, nullptr);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSums));
+    if constexpr (S_::kMoveRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSums));
     // ------------------------------------------------- running sums and output
     const int q = warp & 3;            // TMEM lane quarter this warp may access
     const int part = (warp - 4) / 4;   // its part of the columns
     float* mine = scales + (warp - 4) * 2 * kScaleRows * kScalePitch;
-    // Ask for the scales of blocks [kb, kb + kScaleBlocks) of the tile (e, nt,
-    // mt)'s 32 rows (past the segment's last row, that row's) and columns.
-    auto ask = [&](int e, int nt, int mt, int kb, int b) {
-      __syncwarp();
+    // The scales of a tile's 32 rows (past the segment's last row, that row's)
+    // and of its columns: aim at a tile, then ask for blocks [kb, kb +
+    // kScaleBlocks). Lanes 8 i + j bring block kb + j of rows i, i + 4, ...
+    const int sj = lane % kScaleBlocks, sr = lane / kScaleBlocks;
+    const float *sa = nullptr, *sw = nullptr;
+    int s_last = 0;  // the last of the 32 rows that may be read
+    auto aim = [&](int e, int nt, int mt) {
       const int first = seg[e] + mt * BM + q * 32, last = seg[e + 1] - 1;
-      const int j = lane % kScaleBlocks;
-      float* to = mine + b * kScaleRows * kScalePitch + j;
-      if (kb + j < p.KB) {
+      const int nb = min((nt * kBN + part * kCols) / 128, p.NB - 1);
+      s_last = last - first;
+      sa = p.a_scale + static_cast<int64_t>(first) * p.KB + sj;
+      sw = p.w_scale + (static_cast<int64_t>(e) * p.NB + nb) * p.KB + sj;
+    };
+    auto ask = [&](int kb, int b) {
+      const uint32_t to = smem_u32(mine + b * kScaleRows * kScalePitch + sr * kScalePitch + sj);
+      if (kb + sj < p.KB) {
+        if (s_last >= 31) {
+          const float* from = sa + sr * p.KB + kb;
 #pragma unroll
-        for (int i = 0; i < kScaleBlocks; ++i) {
-          const int r = i * (32 / kScaleBlocks) + lane / kScaleBlocks;
-          cp_async4(smem_u32(to + r * kScalePitch), p.a_scale + static_cast<int64_t>(min(first + r, last)) * p.KB + kb + j);
+          for (int i = 0; i < kScaleBlocks; ++i, from += 4 * p.KB) cp_async4(to + i * (4 * kScalePitch * 4), from);
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < kScaleBlocks; ++i)
+            cp_async4(to + i * (4 * kScalePitch * 4), sa + static_cast<int64_t>(min(i * 4 + sr, s_last)) * p.KB + kb);
         }
-        if (lane < kScaleBlocks) {
-          const int nb = min((nt * kBN + part * kCols) / 128, p.NB - 1);
-          cp_async4(smem_u32(to + 32 * kScalePitch), p.w_scale + (static_cast<int64_t>(e) * p.NB + nb) * p.KB + kb + j);
-        }
+        if (sr == 0) cp_async4(to + 32 * kScalePitch * 4, sw + kb);
       }
       cp_async_commit();
     };
     int buf = 0, sbuf = 0;
     uint32_t buf_phase = 0;
     bool failed = false;
+    const uint32_t from = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + part * kCols;
     int e = 0, nt = 0, mt = 0;
     if (blockIdx.x < total) {
       decode_tile(blockIdx.x, tpre, seg, p.E, BM, e, nt, mt);
-      ask(e, nt, mt, 0, 0);
+      aim(e, nt, mt);
+      ask(0, 0);
     }
     for (int tile = blockIdx.x; tile < total && !failed; tile += gridDim.x) {
       const int row = seg[e] + mt * BM + q * 32 + lane;
       const bool valid = row < seg[e + 1];
       const int n0 = nt * kBN + part * kCols;
-      const int this_e = e, this_nt = nt, this_mt = mt;
-      if (tile + static_cast<int>(gridDim.x) < total) decode_tile(tile + gridDim.x, tpre, seg, p.E, BM, e, nt, mt);
+      const int this_e = e;
+      const bool more = tile + static_cast<int>(gridDim.x) < total;
+      if (more) decode_tile(tile + gridDim.x, tpre, seg, p.E, BM, e, nt, mt);
       // the sums start at the bias, which arrives while the first block is multiplied
       float acc[kCols];
 #pragma unroll
@@ -389,77 +399,43 @@ __global__ void __launch_bounds__(S_::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[c + i] = f[i];
       }
-      for (int kb0 = 0; kb0 < p.KB; kb0 += kU) {
-        if (kb0 % kScaleBlocks == 0) {
+      for (int kb = 0; kb < p.KB; ++kb) {
+        if (kb % kScaleBlocks == 0) {
           // the following blocks' scales, the next tile's first after the last
-          if (kb0 + kScaleBlocks < p.KB)
-            ask(this_e, this_nt, this_mt, kb0 + kScaleBlocks, sbuf ^ 1);
-          else if (tile + static_cast<int>(gridDim.x) < total)
-            ask(e, nt, mt, 0, sbuf ^ 1);
-          else
+          if (kb + kScaleBlocks < p.KB)
+            ask(kb + kScaleBlocks, sbuf ^ 1);
+          else if (more) {
+            aim(e, nt, mt);
+            ask(0, sbuf ^ 1);
+          } else
             cp_async_commit();
           cp_async_wait_1();
           __syncwarp();
           sbuf ^= 1;
         }
-        const int n = min(kU, p.KB - kb0);
-        float s[kU];
-        const float* at = mine + (sbuf ^ 1) * kScaleRows * kScalePitch + kb0 % kScaleBlocks;
+        const float* at = mine + (sbuf ^ 1) * kScaleRows * kScalePitch + kb % kScaleBlocks;
+        const float s = at[lane * kScalePitch] * at[32 * kScalePitch];
+        if (!__all_sync(0xffffffffu, wait_bounded(tfull_bar(buf), buf_phase, abort_flag))) {
+          failed = true;
+          break;
+        }
+        tc_fence_after();
+        uint32_t v[64];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) s[u] = at[lane * kScalePitch + u] * at[32 * kScalePitch + u];
-        const uint32_t from = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + part * kCols;
-        if constexpr (kCols > 64) {
-          if (!__all_sync(0xffffffffu, wait_bounded(tfull_bar(buf), buf_phase, abort_flag))) {
-            failed = true;
-            break;
-          }
-          tc_fence_after();
-          // half of the columns at a time
-          uint32_t v[kLd];
-#pragma unroll
-          for (int c = 0; c < kCols; c += kLd) {
-            tmem_ld_cols(from + buf * kBN + c, v);
-            tmem_ld_wait();
-            if (c + kLd == kCols) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(tempty_bar(buf));
-            }
-#pragma unroll
-            for (int i = 0; i < kLd; i += 2) fma2(acc[c + i], acc[c + i + 1], s[0], v[i], v[i + 1]);
-          }
-          if (++buf == kBufs) {
-            buf = 0;
-            buf_phase ^= 1u;
-          }
-        } else {
-          // kU blocks' sums out of TMEM at once: one wait for their loads
-          uint32_t v[kU][kCols];
-          const int buf0 = buf;
-#pragma unroll
-          for (int u = 0; u < kU; ++u) {
-            if (u < n) {
-              if (!__all_sync(0xffffffffu, wait_bounded(tfull_bar(buf), buf_phase, abort_flag))) failed = true;
-              tc_fence_after();
-#pragma unroll
-              for (int c = 0; c < kCols; c += kLd)
-                tmem_ld_cols(from + buf * kBN + c, *reinterpret_cast<uint32_t(*)[kLd]>(&v[u][c]));
-              if (++buf == kBufs) {
-                buf = 0;
-                buf_phase ^= 1u;
-              }
-            }
-          }
+        for (int c = 0; c < kCols; c += 64) {
+          tmem_ld_x64(from + buf * kBN + c, v);
           tmem_ld_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane < n) mbar_arrive(tempty_bar((buf0 + lane) % kBufs));
-          if (failed) break;
+          if (c + 64 == kCols) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tempty_bar(buf));
+          }
 #pragma unroll
-          for (int u = 0; u < kU; ++u)
-            if (u < n)
-#pragma unroll
-              for (int c = 0; c < kCols; c += 2) fma2(acc[c], acc[c + 1], s[u], v[u][c], v[u][c + 1]);
+          for (int i = 0; i < 64; i += 2) fma2(acc[c + i], acc[c + i + 1], s, v[i], v[i + 1]);
+        }
+        if (++buf == kBufs) {
+          buf = 0;
+          buf_phase ^= 1u;
         }
       }
       if (failed) {
@@ -570,7 +546,7 @@ moe_status_t launch_fp8_matmul(const moe_fp8_t& d, const uint8_t* a, const float
     return us * (rounds < 1.0 ? 1.0 : rounds);
   };
   const double c256 = cost(256, few ? 0.82 : 0.68), c192 = cost(192, 0.64), c64 = cost(64, 0.36);
-  if (c64 <= c192 && c64 <= c256) return launch<Shape<64, 8>>(p, a, w, s);
+  if (c64 <= c192 && c64 <= c256) return launch<Shape<64, 4>>(p, a, w, s);
   if (c192 <= c256) return launch<Shape<192, 12>>(p, a, w, s);
   return launch<Shape<256, 8>>(p, a, w, s);
 }

@@ -131,13 +131,12 @@ __device__ __forceinline__ void mma_bf16_16816(float (&c)[4], uint32_t a0, uint3
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// The same with f16 operands, and with a zero in place of C.
-__device__ __forceinline__ void mma_f16_16816_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                                   uint32_t b0, uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+// The same with f16 operands, D apart from C.
+__device__ __forceinline__ void mma_f16_16816_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                   uint32_t b0, uint32_t b1, const float (&c)[4]) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
@@ -461,7 +460,8 @@ __device__ __forceinline__ void mul_bf16(const uint8_t* slot, int r, int q, int 
 // two rows of codes, s_lo, s_hi: in their scales. All four and b move on.
 template <int kN, int kUnits>
 __device__ __forceinline__ void mul_mx(const uint8_t*& at, const uint8_t*& at8, const uint8_t*& s_lo,
-                                       const uint8_t*& s_hi, const uint8_t* (&b)[kN], float (&acc)[kN][4]) {
+                                       const uint8_t*& s_hi, const uint8_t* (&b)[kN], const float (&zero)[4],
+                                       float (&acc)[kN][4]) {
 #pragma unroll
   for (int j = 0; j < kUnits; ++j) {
     uint32_t a[4], a8[4];
@@ -472,7 +472,7 @@ __device__ __forceinline__ void mul_mx(const uint8_t*& at, const uint8_t*& at8, 
     for (int g = 0; g < kN; ++g) {
       const uint4 v = lds<uint4>(b[g] + j * 64);
       float c[4];
-      mma_f16_16816_zero(c, a[0], a8[0], a[1], a8[1], v.x, v.y);
+      mma_f16_16816_from(c, a[0], a8[0], a[1], a8[1], v.x, v.y, zero);
       mma_f16_16816(c, a[2], a8[2], a[3], a8[3], v.z, v.w);
       acc[g][0] = fmaf(w_lo, c[0], acc[g][0]);
       acc[g][1] = fmaf(w_lo, c[1], acc[g][1]);
@@ -727,6 +727,11 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 : 0), 1) 
     for (int i = 0; i < p.stages; ++i) issue();
   __syncthreads();  // the lists are complete
 
+  // Four registers of zeros that the compiler takes for values: C of every
+  // unit's first MMA, without writing zeros for each.
+  float zero[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) asm volatile("mov.f32 %0, 0f00000000;" : "=f"(zero[i]));
   int slot = 0, it = 0;     // of the ring; turn
   uint32_t slab_phase = 0;  // MXFP4: of the ring
   const int buf_shift = p.red_bufs >> 1;  // log2 of 1, 2 or 4
@@ -853,10 +858,10 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 : 0), 1) 
               const uint8_t* b[kN];
 #pragma unroll
               for (int j = 0; j < kN; ++j) b[j] = brow[j] + (first + u0) * 64;
-              for (; left >= 8; left -= 8) mul_mx<kN, 8>(at, at8, s_lo, s_hi, b, acc);
-              if (left & 4) mul_mx<kN, 4>(at, at8, s_lo, s_hi, b, acc);
-              if (left & 2) mul_mx<kN, 2>(at, at8, s_lo, s_hi, b, acc);
-              if (left & 1) mul_mx<kN, 1>(at, at8, s_lo, s_hi, b, acc);
+              for (; left >= 8; left -= 8) mul_mx<kN, 8>(at, at8, s_lo, s_hi, b, zero, acc);
+              if (left & 4) mul_mx<kN, 4>(at, at8, s_lo, s_hi, b, zero, acc);
+              if (left & 2) mul_mx<kN, 2>(at, at8, s_lo, s_hi, b, zero, acc);
+              if (left & 1) mul_mx<kN, 1>(at, at8, s_lo, s_hi, b, zero, acc);
             }
             __syncwarp();
             if (lane == 0) sm100::mbar_arrive(sm100::smem_u32(&sh.w_empty[slot]));

@@ -495,56 +495,54 @@ template <int kFmt>
 __device__ __forceinline__ void load_rows(const FewParams& p, FewShared& sh, const uint16_t* from, int rows, int K,
                                           uint8_t* act) {
   const int per = K / 8;  // 16-byte chunks per row
-  const int total = rows * per;
-  constexpr int kAtOnce = 4;  // loads in flight per thread
-  for (int base = threadIdx.x & ~31; base < total; base += kAtOnce * kThreads) {  // (uniform in a warp)
-    uint4 v[kAtOnce];
+  constexpr int kAtOnce = 4;  // rows in flight
+  for (int n0 = 0; n0 < rows; n0 += kAtOnce) {
+    for (int base = threadIdx.x & ~31; base < per; base += kThreads) {  // (uniform in a warp)
+      const int c = base + (threadIdx.x & 31);
+      uint4 v[kAtOnce];
 #pragma unroll
-    for (int z = 0; z < kAtOnce; ++z) {
-      const int i = base + z * kThreads + (threadIdx.x & 31);
-      v[z] = i < total ? __ldcg(reinterpret_cast<const uint4*>(from) + i) : make_uint4(0, 0, 0, 0);
-    }
+      for (int z = 0; z < kAtOnce; ++z)
+        v[z] = n0 + z < rows && c < per
+                   ? __ldcg(reinterpret_cast<const uint4*>(from) + static_cast<int64_t>(n0 + z) * per + c)
+                   : make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int z = 0; z < kAtOnce; ++z) {
-      const int first = base + z * kThreads, i = first + (threadIdx.x & 31);
-      if (first >= total) break;
-      const int n = min(i, total - 1) / per, c = i - n * per;
-      if (i < total) *reinterpret_cast<uint4*>(act + n * p.row_pitch + c * 16) = v[z];
-      if (kFmt == MOE_W_MXFP4) {
-        const uint32_t w[4] = {v[z].x, v[z].y, v[z].z, v[z].w};
-        uint32_t m = 0;
+      for (int z = 0; z < kAtOnce; ++z) {
+        if (n0 + z >= rows) break;
+        if (c < per) *reinterpret_cast<uint4*>(act + (n0 + z) * p.row_pitch + c * 16) = v[z];
+        if (kFmt == MOE_W_MXFP4) {
+          const uint32_t w[4] = {v[z].x, v[z].y, v[z].z, v[z].w};
+          uint32_t m = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) m = max(m, max(w[j] & 0x7fffu, (w[j] >> 16) & 0x7fffu));
-        // a warp's chunks are consecutive: mostly of one row, then one atomic
-        if (__shfl_sync(0xffffffffu, n, 0) == __shfl_sync(0xffffffffu, n, 31)) {
+          for (int j = 0; j < 4; ++j) m = max(m, max(w[j] & 0x7fffu, (w[j] >> 16) & 0x7fffu));
           m = __reduce_max_sync(0xffffffffu, m);
-          if ((threadIdx.x & 31) == 0) atomicMax(&sh.row_max[n], m);
-        } else {
-          atomicMax(&sh.row_max[n], m);
+          if ((threadIdx.x & 31) == 0) atomicMax(&sh.row_max[n0 + z], m);
         }
       }
     }
   }
   if (kFmt == MOE_W_MXFP4) {
     warps_sync();
-    for (int i = threadIdx.x; i < total; i += kThreads) {
-      const int n = i / per, c = i - n * per;
+    for (int n = 0; n < rows; ++n) {
       // 2^shift brings the row's largest magnitude into [2^8, 2^9); a row of
       // zeros, or with an infinity or NaN, stays as it is
-      const int ex = static_cast<int>(sh.row_max[n] >> 7);  // biased exponent
-      const int shift = sh.row_max[n] == 0 || ex == 255 ? 0 : min(127, 8 + 127 - max(ex, 1));
+      const uint32_t largest = sh.row_max[n];
+      const int ex = static_cast<int>(largest >> 7);  // biased exponent
+      const int shift = largest == 0 || ex == 255 ? 0 : min(127, 8 + 127 - max(ex, 1));
       const float mul = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
-      if (c == 0) sh.row_scale[n] = __uint_as_float(shift == 127 ? 0x00400000u : static_cast<uint32_t>(127 - shift) << 23);
-      uint4* at = reinterpret_cast<uint4*>(act + n * p.row_pitch + c * 16);
-      const uint4 v = *at;
-      uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      if (threadIdx.x == 0)
+        sh.row_scale[n] = __uint_as_float(shift == 127 ? 0x00400000u : static_cast<uint32_t>(127 - shift) << 23);
+      for (int c = threadIdx.x; c < per; c += kThreads) {
+        uint4* at = reinterpret_cast<uint4*>(act + n * p.row_pitch + c * 16);
+        const uint4 v = *at;
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int z = 0; z < 4; ++z) {
-        const __half2 h2 = __floats2half2_rn(__uint_as_float(w[z] << 16) * mul,
-                                             __uint_as_float(w[z] & 0xffff0000u) * mul);
-        w[z] = *reinterpret_cast<const uint32_t*>(&h2);
+        for (int z = 0; z < 4; ++z) {
+          const __half2 h2 = __floats2half2_rn(__uint_as_float(w[z] << 16) * mul,
+                                               __uint_as_float(w[z] & 0xffff0000u) * mul);
+          w[z] = *reinterpret_cast<const uint32_t*>(&h2);
+        }
+        *at = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      *at = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
@@ -760,60 +758,77 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 : 0), 1) 
         const int n = min(8 * i + fr, rows - 1);
         brow[i] = act + (which == 1 ? nth_bit(sh.tokens[e], n) : n) * p.row_pitch + (kFmt == MOE_W_BF16 ? s.u0 * 64 : 0) + fq * 16;
       }
-      // Finish the granules that began at `first`, in turn `turn`: 4 kN tasks
-      // of 128 sums each, spread over the warps.
+      // A turn's granules are finished by `tasks` warps' worth of work, 128 sums
+      // each; a warp always has the same tasks (every turn, or every second or
+      // fourth where there are fewer tasks than warps), so what they need is
+      // worked out once for the expert.
       constexpr int kTasks = kN;  // at most, of a warp
+      struct Task {
+        bool mine, on;       // there is one; its sum is of a token that is there
+        int m;               // granule of the turn
+        const float* part;   // first of the sums' parts, in the first buffer
+        float scale, gate;
+        const uint16_t* bias;
+        int64_t out;         // element of h or o, for granule 0
+      } task[kTasks];
       uint16_t bias[kTasks];
-      auto task_of = [&](int i, int turn) { return ((warp - turn * tasks) & (kWarps - 1)) + kWarps * i; };
+#pragma unroll
+      for (int i = 0; i < kTasks; ++i) {
+        const int id = (warp & (tasks - 1)) + kWarps * i;
+        const int grp = id / 4 % kN, at = (id % 4) * 32 + lane;
+        // fragment element -> weight row r and token n
+        const int r = at / 16 + (at & 2 ? 8 : 0), n = 8 * grp + (at / 4 % 4) * 2 + (at & 1);
+        task[i].mine = id < tasks;
+        task[i].m = id / (4 * kN);
+        task[i].on = task[i].mine && n < rows;
+        const int row = start + (n < rows ? n : 0), a = sh.slot[row];
+        task[i].part = red + (task[i].m * split * kN + grp) * 128 + at;
+        task[i].scale = kFmt == MOE_W_BF16 ? 1.0f : sh.row_scale[which == 1 ? a / p.k : row - start];
+        task[i].gate = sh.gate[a / p.k][a % p.k];
+        task[i].bias = which == 1 ? p.b1 + static_cast<int64_t>(e) * 2 * p.I + (r < 8 ? r : p.I + r - 8)
+                                  : p.b2 + static_cast<int64_t>(e) * p.D + r;
+        task[i].out = which == 1 ? static_cast<int64_t>(row) * p.I + r : static_cast<int64_t>(a) * p.D + r;
+        if (which == 1 && r >= 8) task[i].on = false;  // an up half: its gate's lane writes h
+      }
+      auto my_turn = [&](int turn) { return tasks >= kWarps || warp / tasks == (turn & (kWarps / tasks - 1)); };
       // What the finish needs from memory, asked for a turn ahead.
       auto load_bias = [&](int first, int turn) {
+        if (!my_turn(turn)) return;
 #pragma unroll
         for (int i = 0; i < kTasks; ++i) {
-          const int task = task_of(i, turn), local = first + task / (4 * kN), at = (task % 4) * 32 + lane;
-          const int r = at / 16 + (at & 2 ? 8 : 0);
-          bias[i] = 0;
-          if (task < tasks && local < end)
-            bias[i] = which == 1 ? p.b1[static_cast<int64_t>(e) * 2 * p.I + local * 8 + (r < 8 ? r : p.I + r - 8)]
-                                 : p.b2[static_cast<int64_t>(e) * p.D + local * 16 + r];
+          const int local = first + task[i].m;
+          if (task[i].mine && local < end) bias[i] = task[i].bias[local * s.step];
         }
       };
       auto finish = [&](int first, int turn) {
         const int buf = turn & (p.red_bufs - 1);
-        const float* part = red + buf * kRedFloats;
-        wait_local(full_at + 8 * buf, (turn >> buf_shift) & 1, p.header);
+        const bool active = my_turn(turn);
         float sum[kTasks];
+        if (active) {
+          wait_local(full_at + 8 * buf, (turn >> buf_shift) & 1, p.header);
 #pragma unroll
-        for (int i = 0; i < kTasks; ++i) {
-          const int task = task_of(i, turn);
-          sum[i] = 0.0f;
-          if (task < tasks) {
-            const int m = task / (4 * kN), grp = task / 4 % kN, at = (task % 4) * 32 + lane;
+          for (int i = 0; i < kTasks; ++i) {
+            sum[i] = 0.0f;
+            if (task[i].mine) {
+              const float* part = task[i].part + buf * kRedFloats;
 #pragma unroll 4
-            for (int w = 0; w < split; ++w)
-              sum[i] += part[((m * split + w) * kN + grp) * 128 + at];
+              for (int w = 0; w < split; ++w) sum[i] += part[w * (kN * 128)];
+            }
           }
+          __syncwarp();
         }
-        __syncwarp();
         if (lane == 0) sm100::mbar_arrive(empty_at + 8 * buf);
+        if (!active) return;
 #pragma unroll
         for (int i = 0; i < kTasks; ++i) {
-          const int task = task_of(i, turn), local = first + task / (4 * kN);
-          if (task >= tasks || local >= end) continue;  // (uniform in a warp)
-          const int grp = task / 4 % kN, at = (task % 4) * 32 + lane;
-          // fragment element -> weight row r and token n
-          const int r = at / 16 + (at & 2 ? 8 : 0), n = 8 * grp + (at / 4 % 4) * 2 + (at & 1);
-          const bool on = n < rows;
-          const int row = start + (on ? n : 0);
-          const uint32_t a = sh.slot[row];
-          float v = sum[i];
-          if (kFmt == MOE_W_MXFP4) v *= sh.row_scale[which == 1 ? a / p.k : on ? n : 0];
-          v += bf16_bits_to_float(bias[i]);
+          const int local = first + task[i].m;
+          if (!task[i].mine || local >= end) continue;  // (uniform in a warp)
+          const float v = fmaf(sum[i], task[i].scale, bf16_bits_to_float(bias[i]));
           if (which == 1) {
             const float up = __shfl_xor_sync(0xffffffffu, v, 2);
-            if (on && r < 8)
-              p.h[static_cast<int64_t>(row) * p.I + local * 8 + r] = float_to_bf16_bits(glu_act(v, up, p.act));
-          } else if (on) {
-            p.o[static_cast<int64_t>(a) * p.D + local * 16 + r] = sh.gate[a / p.k][a % p.k] * v;
+            if (task[i].on) p.h[task[i].out + local * 8] = float_to_bf16_bits(glu_act(v, up, p.act));
+          } else if (task[i].on) {
+            p.o[task[i].out + local * 16] = task[i].gate * v;
           }
         }
       };

@@ -70,7 +70,7 @@ def _run(R, E, N, K, offsets, dtype, bias=True, seed=0):
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("R,N,K", [(1, 16, 16), (1, 2880, 2880), (17, 272, 144), (32, 128, 128), (33, 64, 256),
                                    (128, 256, 128), (129, 400, 1040), (300, 2880, 2880), (1000, 528, 528),
-                                   (513, 1040, 4096)])
+                                   (513, 1040, 4096), (2100, 5760, 272)])  # (the last: 256-column tiles)
 def test_dense(R, N, K, dtype):
     out = _run(R, 1, N, K, [0, R], dtype, bias=R != 128)
     a, a_scale, w, w_scale, b = _make(R, 1, N, K, R + 1, R != 128)
@@ -87,6 +87,9 @@ def test_dense(R, N, K, dtype):
     ([700, 0, 257, 1], 272, 656, 5),              # wide tiles
     ([0, 0, 0], 64, 64, 4),                       # no rows at all in any segment
     ([2] * 256, 64, 128, 0),                      # the most experts
+    ([400, 390, 0, 1, 600, 129, 128, 500], 2880, 144, 7),  # 256 columns
+    ([1500, 0, 701], 4112, 400, 3),               # ragged in rows and columns
+    ([0, 1793, 257, 1], 5120, 160, 0),
 ])
 def test_grouped(counts, N, K, extra, dtype):
     offsets = [0]

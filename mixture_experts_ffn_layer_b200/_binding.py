@@ -109,13 +109,13 @@ def dims(T, D, E, k, I, wfmt=MOE_W_BF16, act=MOE_ACT_SWIGLU, act_alpha=1.0, act_
 
 
 def _p(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
     if stream is None:  # (the raw handle: building a torch.cuda.Stream around it takes longer than a small launch)
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _w(data: Optional[torch.Tensor], scales: Optional[torch.Tensor] = None,

@@ -45,7 +45,7 @@ def _like(out: Optional[torch.Tensor], of: Optional[torch.Tensor], dtype, what: 
         _require(out is None, f"{what} without a residual")
         return None
     if out is None:
-        return of.new_empty(of.shape)
+        return torch.empty_like(of)
     _require(out.shape == of.shape and out.dtype == dtype and out.is_contiguous() and out.device == of.device,
              f"{what} must be a contiguous (T, D) tensor of its input's type, on its device")
     return out
@@ -71,7 +71,7 @@ def rmsnorm_fp8(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-5, residua
     per row and 128 columns."""
     n = _norm_dims(x, gamma, eps, residual)
     T, D = x.shape
-    q = x.new_empty((T, D), dtype=torch.float8_e4m3fn)
+    q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
     scale = x.new_empty((T, -(-D // 128)), dtype=torch.float32)
     res = _like(res_out, residual, None if residual is None else residual.dtype, "res_out")
     _on(x.device, B.moe_rmsnorm, n, x, residual, gamma, res, None, q, scale, stream)

@@ -79,8 +79,10 @@ class MoELayer:
         """forward for at most few_max_tokens tokens in one launch
         (moe_forward_few): the latency path of a decode step. MXFP4 weights
         are read as stored, so the layer keeps their codes and scales."""
+        if x.dim() != 2 or x.shape[1] != self.D or x.dtype != torch.bfloat16 or not x.is_contiguous():
+            raise ValueError("x must be a contiguous (T, D) bf16 tensor")
         T = x.shape[0]
-        y = out if out is not None else torch.empty((T, self.D), dtype=torch.bfloat16, device=x.device)
+        y = out if out is not None else torch.empty_like(x)
         moe_forward_few(self.dims(T), x, self.Wr, self.br, self.W1, self.b1, self.W2, self.b2, y, self.workspace(T),
                         W1_scales=self.W1_scales, W2_scales=self.W2_scales, stream=stream)
         return y

@@ -298,7 +298,9 @@ moe_status_t moe_rmsnorm(moe_norm_t n, const uint16_t* x, const void* residual, 
 moe_status_t moe_check_fp8(moe_fp8_t d) {
   if (d.R < 0 || d.E <= 0 || d.N <= 0 || d.K <= 0) return MOE_ERR_INVALID_ARG;
   if (d.out_type != MOE_T_BF16 && d.out_type != MOE_T_F32) return MOE_ERR_INVALID_ARG;
-  if (d.E > 256 || d.N % 16 || d.K % 16 || d.N > 65536 || d.K > 65536) return MOE_ERR_UNSUPPORTED;
+  if (d.E > 256 || d.N % 16 || d.K % 16 || d.N > 65536 || d.K > 65536 || d.R > (1 << 30)) return MOE_ERR_UNSUPPORTED;
+  // the kernel numbers its tiles (at least 64 columns wide) in 32 bits
+  if ((int64_t{d.R} / 128 + 1 + d.E) * ((d.N + 63) / 64) >= int64_t{1} << 31) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

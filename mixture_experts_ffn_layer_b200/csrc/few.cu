@@ -21,30 +21,43 @@
 // and each warp meets the same slice of the activations in every granule.
 // The rings run on across granules, experts and from mlp1 into mlp2, whose
 // first weights arrive while the grid barrier is waited for. The multiplication
-// is mma.sync m16n8k16: the 16 weight
-// rows are M, up to 8 tokens are N (two N halves for more than 8). That is
-// the shape this work has -- a 128-row tensor tile would leave the SMs unevenly
-// loaded -- and the tensor rate is far from being a limit. The k index of an
-// MMA is permuted (lane q of a row's four holds 8 consecutive elements of a
-// 32-element unit), the same for weights and activations, so both are read
-// with wide shared-memory loads. The warps' partial sums meet in shared memory
-// behind mbarriers (full / empty per buffer): a few warps, taking turns, add
-// them in warp order and finish the granule while the others go on.
+// is mma.sync m16n8k16: the 16 weight rows are M, up to 8 tokens are N (two N
+// halves for more than 8). That is the shape this work has -- a 128-row tensor
+// tile would leave the SMs unevenly loaded -- and the tensor rate is far from
+// being a limit. The k index of an MMA is permuted (lane q of a row's four holds
+// 8 consecutive elements of a 32-element unit), the same for weights and
+// activations, so both are read with wide shared-memory loads. The warps' partial
+// sums meet in shared memory behind mbarriers (full / empty per buffer): some of
+// the warps add them in warp order and finish the granule a turn later.
 //
-// bf16: each warp streams its own slices through its own cp.async ring, with
-// no synchronisation between the warps to load.
+// bf16: each warp streams its own slices through its own cp.async ring, with no
+// synchronisation between the warps to load.
 //
 // MXFP4: the granules are a quarter of the size and the work on a byte four
-// times as much, so what counts is instructions: a 17th warp brings whole
-// granules in by bulk copies (no instruction of the 16 is spent on loads), and
-// where a block has enough of them the warps work on up to four granules at a
-// time, 16 / that many on each, which leaves fewer partial sums to add. A unit
-// of 32 codes is one scale block. The codes become f16 (exact), the activations f16 with one power of two per row such that the largest
-// magnitude is in [2^8, 2^9) (exact down to 2^-25 of it, absolute error below
-// 2^-33 of it), and each unit's fp32 sum is added with its weight scale.
+// times as much, so instructions and hand-overs count: other warps bring pairs
+// of granules in by bulk copies (the 16 spend nothing on loads), and the warps
+// work on two or four granules at a time, 16 / that many on each, which leaves
+// fewer partial sums to add. A unit of 32 codes is one scale block. The codes
+// become f16 (exact), the activations f16 with one power of two per row such that
+// the largest magnitude is in [2^8, 2^9) (exact down to 2^-25 of it, absolute
+// error below 2^-33 of it), and each unit's fp32 sum is added with its weight
+// scale.
 //
 // All sums are fp32. The order is fixed by the sizes, so results are bitwise
 // reproducible.
+//
+// Measured, D = I = 2880, top-4 (the weights' bytes at the measured copy rate in
+// brackets; a kernel that only reads needs 36 us for one token's 199 MB of bf16
+// weights and about 15 for its 53 MB of MXFP4): 32 experts, bf16, 1 token 48 us
+// (30), 16 tokens 250 (224); MXFP4, 1 token 28 us (8); 128 experts, MXFP4, 7
+// tokens 98 us (54). What is left: about 7 us in front of the weights (router,
+// barrier, lists), 2.5 us at each later barrier, and for MXFP4 the codes'
+// conversion and multiplication, which take as long as the memory does and overlap
+// it only in part. Measured and not kept: 24 warps for MXFP4 (72 registers: no
+// faster), two granules per warp sharing the activations' loads (mlp1 41 -> 49
+// us), row-by-row copies of the codes (60 ns each: 49 -> 60), a router worked out
+// by every block in place of the first barrier (4.1 -> 10.9 us: every SM reads the
+// same weights from cold).
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -56,7 +69,8 @@
 namespace moe {
 namespace {
 
-constexpr int kWarps = 16;
+constexpr int kWarps = 16;             // that compute
+constexpr int kLoaders = 4;            // that load, in an MXFP4 block
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxT = 16;
 constexpr int kMaxK = 8;
@@ -161,8 +175,10 @@ __device__ __forceinline__ void e2m1_to_f16(uint32_t codes, uint32_t (&p)[4]) {
 // E8M0: 2^(s - 127); the smallest, 2^-127, counts as zero.
 __device__ __forceinline__ float e8m0(uint32_t s) { return __uint_as_float(s << 23); }
 
-// The 16 computing warps meet (an MXFP4 block has a 17th, which loads).
+// The 16 computing warps meet (an MXFP4 block has more, which load).
 __device__ __forceinline__ void warps_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+
+__device__ __forceinline__ void loaders_sync() { asm volatile("bar.sync 2, %0;" ::"n"(32 * kLoaders) : "memory"); }
 
 // All blocks of the grid meet (the launch is cooperative, so all are
 // resident). Waits at most kBarrierNs, then records the timeout and goes on:
@@ -360,20 +376,25 @@ __host__ __device__ constexpr int mx_stage_bytes(int units, int nchunks) {
   return (32 * (mx_pitch(units, nchunks, (units + nchunks - 1) / nchunks) + units) + 127) / 128 * 128;
 }
 
-// The loading warp of an MXFP4 block: mlp1's granules then mlp2's, turn by
+// The loading warps of an MXFP4 block: mlp1's granules then mlp2's, turn by
 // turn, two granules a stage. Of W1 rows 0..15 of a stage are gate rows and
-// 16..31 the up rows.
+// 16..31 the up rows. The first warp does it alone where the codes are copied as
+// they lie; row by row each of the four copies its quarter of the rows (four
+// issuers of bulk copies reach twice the rate of one).
 __device__ __forceinline__ void mx_produce(const FewParams& p, FewShared& sh, const Stream& st1, const Stream& st2,
-                                           uint32_t ring, int lane) {
+                                           uint32_t ring, int loader, int lane) {
   using namespace sm100;
   const uint32_t full = smem_u32(sh.w_full), empty = smem_u32(sh.w_empty);
   int slot = 0, issued = 0;
   uint32_t phase = 0;
   bool failed = false;
-  for (int which = 1; which <= 2 && !failed; ++which) {
+  for (int which = 1; which <= 2; ++which) {
+    // (the other loaders have not followed the ring's phases through a weight
+    // that the first copies alone: they go on from where it stands)
+    if (which == 2) loaders_sync();
     const Stream& st = which == 1 ? st1 : st2;
     const int pitch = mx_pitch(st.units, st.nchunks, st.chunk);
-    const bool as_stored = mx_as_stored(st.units, st.nchunks);
+    const bool as_stored = mx_as_stored(st.units, st.nchunks), idle = as_stored && loader != 0;
     int ai = st.g0 / st.per_expert, local = st.g0 % st.per_expert, in_turn = 0;
     for (int g = st.g0; g < st.g1 && !failed;) {
       const int left = min(st.per_expert - local, st.g1 - g);  // of this expert
@@ -384,24 +405,25 @@ __device__ __forceinline__ void mx_produce(const FewParams& p, FewShared& sh, co
       const uint8_t* w = (which == 1 ? p.w1 : p.w2) + row0 * st.row_bytes;
       const uint8_t* s = (which == 1 ? p.s1 : p.s2) + row0 * st.srow_bytes;
       for (int c = 0; c < st.nchunks; ++c) {
-        if (!wait_bounded(empty + 8 * slot, phase ^ 1u)) {
+        if (!idle && !wait_bounded(empty + 8 * slot, phase ^ 1u)) {
           failed = true;
           break;
         }
         const int n = min(st.chunk, st.units - c * st.chunk);
         const uint32_t bar = full + 8 * slot, to = ring + slot * p.slab_bytes;
-        if (lane == 0) mbar_arrive_expect_tx(bar, 16 * count * (n * 16 + st.srow_bytes));
+        if (loader == 0 && lane == 0) mbar_arrive_expect_tx(bar, 16 * count * (n * 16 + st.srow_bytes));
         __syncwarp();
-        if (lane < runs)
+        if (loader == 0 && lane < runs)
           bulk_load(to + 32 * pitch + lane * 16 * st.srow_bytes, s + static_cast<int64_t>(lane) * st.up * st.srow_bytes,
                     run * st.srow_bytes, bar);
         if (as_stored) {
-          if (lane < runs)
+          if (loader == 0 && lane < runs)
             bulk_load(to + lane * 16 * pitch, w + lane * st.up * st.row_bytes, run * pitch, bar);
         } else {
-          const int r = lane % run, wr = r + lane / run * st.up;  // (W2: lanes past its rows have none)
-          if (lane < runs * run)
-            bulk_load(to + (lane / run * 16 + r) * pitch, w + wr * st.row_bytes + c * st.chunk * 16, n * 16, bar);
+          const int i = lane * kLoaders + loader, r = i % run;  // the lane's row, of the first 8 lanes
+          if (i < runs * run)
+            bulk_load(to + (i / run * 16 + r) * pitch, w + (r + i / run * st.up) * st.row_bytes + c * st.chunk * 16, n * 16,
+                      bar);
         }
         ++issued;
         if (++slot == p.stages) {
@@ -434,11 +456,11 @@ __device__ __forceinline__ void mx_produce(const FewParams& p, FewShared& sh, co
   }
 }
 
-// acc (kN groups of 8 tokens) += 16 weight rows x n <= 2 units of a bf16 stage.
+// acc (the first kG of kN groups of 8 tokens) += 16 weight rows x n <= 2 units of a bf16 stage.
 // Two units of a row are 8 pieces of 16 bytes: piece 4 j + q, the halves
 // exchanged in odd rows (conflict-free). `b`: the lane's place in its rows of
 // the activations.
-template <int kN>
+template <int kG, int kN>
 __device__ __forceinline__ void mul_bf16(const uint8_t* slot, int r, int q, int n, const uint8_t* const (&b)[kN],
                                          float (&acc)[kN][4]) {
 #pragma unroll
@@ -447,7 +469,7 @@ __device__ __forceinline__ void mul_bf16(const uint8_t* slot, int r, int q, int 
       const uint8_t* at = slot + r * kBfPitch + (((4 * j + q) ^ ((r & 1) << 2)) * 16);
       const uint4 a = lds<uint4>(at), a8 = lds<uint4>(at + 8 * kBfPitch);
 #pragma unroll
-      for (int g = 0; g < kN; ++g) {
+      for (int g = 0; g < kG; ++g) {
         const uint4 v = lds<uint4>(b[g] + j * 64);
         mma_bf16_16816(acc[g], a.x, a8.x, a.y, a8.y, v.x, v.y);
         mma_bf16_16816(acc[g], a.z, a8.z, a.w, a8.w, v.z, v.w);
@@ -458,7 +480,7 @@ __device__ __forceinline__ void mul_bf16(const uint8_t* slot, int r, int q, int 
 
 // The same for kUnits units of MXFP4 codes; at, at8: the lane's place in its
 // two rows of codes, s_lo, s_hi: in their scales. All four and b move on.
-template <int kN, int kUnits>
+template <int kG, int kUnits, int kN>
 __device__ __forceinline__ void mul_mx(const uint8_t*& at, const uint8_t*& at8, const uint8_t*& s_lo,
                                        const uint8_t*& s_hi, const uint8_t* (&b)[kN], const float (&zero)[4],
                                        float (&acc)[kN][4]) {
@@ -469,7 +491,7 @@ __device__ __forceinline__ void mul_mx(const uint8_t*& at, const uint8_t*& at8, 
     e2m1_to_f16(lds<uint32_t>(at8 + j * 16), a8);
     const float w_lo = e8m0(lds<uint8_t>(s_lo + j)), w_hi = e8m0(lds<uint8_t>(s_hi + j));
 #pragma unroll
-    for (int g = 0; g < kN; ++g) {
+    for (int g = 0; g < kG; ++g) {
       const uint4 v = lds<uint4>(b[g] + j * 64);
       float c[4];
       mma_f16_16816_from(c, a[0], a8[0], a[1], a8[1], v.x, v.y, zero);
@@ -485,7 +507,7 @@ __device__ __forceinline__ void mul_mx(const uint8_t*& at, const uint8_t*& at8, 
   s_lo += kUnits;
   s_hi += kUnits;
 #pragma unroll
-  for (int g = 0; g < kN; ++g) b[g] += kUnits * 64;
+  for (int g = 0; g < kG; ++g) b[g] += kUnits * 64;
 }
 
 // Bring `rows` rows of K bf16 into shared memory; MXFP4 rows become f16
@@ -554,7 +576,7 @@ __device__ __forceinline__ int nth_bit(uint32_t mask, int n) {
 }
 
 template <int kFmt, int kN>
-__global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 : 0), 1) few_kernel(const FewParams p) {
+__global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoaders : 0), 1) few_kernel(const FewParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   // resident rows | partial sums | rings
   uint8_t* act = smem;
@@ -574,10 +596,10 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 : 0), 1) 
       }
       sm100::fence_mbar_init();
     }
-    if (warp == kWarps) {
+    if (warp >= kWarps) {
       __syncthreads();  // the lists are complete
       mx_produce(p, sh, make_stream<kFmt>(p, 1, sh.n_active, 0), make_stream<kFmt>(p, 2, sh.n_active, 0),
-                 sm100::smem_u32(ring), lane);
+                 sm100::smem_u32(ring), warp - kWarps, lane);
       return;
     }
   }
@@ -764,7 +786,7 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 : 0), 1) 
       // worked out once for the expert.
       constexpr int kTasks = kN;  // at most, of a warp
       struct Task {
-        bool mine, on;       // there is one; its sum is of a token that is there
+        bool mine, on;       // there is one, of a group with tokens; this lane's sum is of one of them
         int m;               // granule of the turn
         const float* part;   // first of the sums' parts, in the first buffer
         float scale, gate;
@@ -778,7 +800,7 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 : 0), 1) 
         const int grp = id / 4 % kN, at = (id % 4) * 32 + lane;
         // fragment element -> weight row r and token n
         const int r = at / 16 + (at & 2 ? 8 : 0), n = 8 * grp + (at / 4 % 4) * 2 + (at & 1);
-        task[i].mine = id < tasks;
+        task[i].mine = id < tasks && 8 * grp < rows;
         task[i].m = id / (4 * kN);
         task[i].on = task[i].mine && n < rows;
         const int row = start + (n < rows ? n : 0), a = sh.slot[row];
@@ -846,7 +868,10 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 : 0), 1) 
             const uint8_t* b[kN];
 #pragma unroll
             for (int i = 0; i < kN; ++i) b[i] = brow[i] + u * 64;
-            mul_bf16<kN>(ring_mine + slot * kBfSlot, fr, fq, s.u1 - s.u0 - u, b, acc);
+            if (kN == 1 || rows <= 8)
+              mul_bf16<1>(ring_mine + slot * kBfSlot, fr, fq, s.u1 - s.u0 - u, b, acc);
+            else
+              mul_bf16<kN>(ring_mine + slot * kBfSlot, fr, fq, s.u1 - s.u0 - u, b, acc);
             __syncwarp();
             issue();
             if (++slot == p.stages) slot = 0;
@@ -873,10 +898,15 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 : 0), 1) 
               const uint8_t* b[kN];
 #pragma unroll
               for (int j = 0; j < kN; ++j) b[j] = brow[j] + (first + u0) * 64;
-              for (; left >= 8; left -= 8) mul_mx<kN, 8>(at, at8, s_lo, s_hi, b, zero, acc);
-              if (left & 4) mul_mx<kN, 4>(at, at8, s_lo, s_hi, b, zero, acc);
-              if (left & 2) mul_mx<kN, 2>(at, at8, s_lo, s_hi, b, zero, acc);
-              if (left & 1) mul_mx<kN, 1>(at, at8, s_lo, s_hi, b, zero, acc);
+              if (kN == 1 || rows <= 8) {
+                for (; left >= 8; left -= 8) mul_mx<1, 8>(at, at8, s_lo, s_hi, b, zero, acc);
+                if (left & 4) mul_mx<1, 4>(at, at8, s_lo, s_hi, b, zero, acc);
+                if (left & 2) mul_mx<1, 2>(at, at8, s_lo, s_hi, b, zero, acc);
+                if (left & 1) mul_mx<1, 1>(at, at8, s_lo, s_hi, b, zero, acc);
+              } else {
+                for (; left >= 4; left -= 4) mul_mx<kN, 4>(at, at8, s_lo, s_hi, b, zero, acc);
+                for (; left > 0; --left) mul_mx<kN, 1>(at, at8, s_lo, s_hi, b, zero, acc);
+              }
             }
             __syncwarp();
             if (lane == 0) sm100::mbar_arrive(sm100::smem_u32(&sh.w_empty[slot]));
@@ -892,7 +922,8 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 : 0), 1) 
         if (it >= p.red_bufs) wait_local(empty_at + 8 * buf, ((it >> buf_shift) - 1) & 1, p.header);
 #pragma unroll
         for (int i = 0; i < kN; ++i)
-          *reinterpret_cast<float4*>(part + (warp * kN + i) * 128 + lane * 4) =
+          if (i == 0 || rows > 8)
+            *reinterpret_cast<float4*>(part + (warp * kN + i) * 128 + lane * 4) =
               make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
         __syncwarp();
         if (lane == 0) sm100::mbar_arrive(full_at + 8 * buf);
@@ -957,7 +988,7 @@ moe_status_t launch(FewParams p, cudaStream_t s) {
     return MOE_ERR_CUDA;
   void* args[] = {&p};
   if (cudaLaunchCooperativeKernel(reinterpret_cast<void*>(few_kernel<kFmt, kN>), dim3(num_sms()),
-                                  dim3(kThreads + (mx ? 32 : 0)), args,
+                                  dim3(kThreads + (mx ? 32 * kLoaders : 0)), args,
                                   smem, s) != cudaSuccess) {
     cudaGetLastError();
     return MOE_ERR_CUDA;

@@ -90,7 +90,8 @@ def test_fp8_sizes_and_arguments():
     assert moe.fp8_workspace_bytes(D(5, 3, 64, 64)) >= 4
     for bad, code in ((D(-1, 1, 64, 64), 1), (D(4, 0, 64, 64), 1), (D(4, 1, 0, 64), 1), (D(4, 1, 64, -16), 1),
                       (_binding.Fp8Dims(4, 1, 64, 64, 2), 1), (D(4, 257, 64, 64), 2), (D(4, 1, 72, 64), 2),
-                      (D(4, 1, 64, 72), 2), (D(4, 1, 65552, 64), 2), (D(4, 1, 64, 65552), 2)):
+                      (D(4, 1, 64, 72), 2), (D(4, 1, 65552, 64), 2), (D(4, 1, 64, 65552), 2),
+                      (D((1 << 30) + 1, 1, 64, 64), 2), (D(1 << 30, 1, 65536, 16), 2)):
         assert lib.moe_check_fp8(bad) == code
         with pytest.raises(moe.MoeError):
             moe.fp8_workspace_bytes(bad)

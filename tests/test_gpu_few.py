@@ -63,6 +63,8 @@ def _make(T, D, E, k, I, wfmt, seed=0):
     (16, 4096, 4, 2, 128, SWIGLU),      # the most resident activations: 16 x 4096
     (4, 16384, 2, 1, 64, SWIGLU),       # the longest reductions, several stages per granule
     (3, 64, 3, 2, 16384, GPTOSS),
+    (7, 2880, 8, 2, 512, SWIGLU),       # MXFP4: W1's rows copied as they lie, W2's one by one
+    (13, 512, 8, 2, 704, GPTOSS),       # and the other way round
 ])
 def test_shapes(T, D, E, k, I, act, wfmt):
     inp = _make(T, D, E, k, I, wfmt)
@@ -79,6 +81,19 @@ def test_every_token_count(wfmt):
         inp = dataclasses.replace(full, shape=dataclasses.replace(full.shape, T=T), x=full.x[:T].contiguous())
         y, ws = _few(inp)
         _close(y, ref[:T])
+
+
+@pytest.mark.parametrize("wfmt", ["bf16", "mxfp4"])
+def test_experts_with_few_and_with_many_tokens(wfmt):
+    # one expert takes every token (two groups of 8), the others a few (one)
+    inp = _make(16, 448, 24, 3, 320, wfmt)
+    br = torch.zeros(24)
+    br[11] = 30.0
+    inp = dataclasses.replace(inp, br=br.to(BF16).cuda())
+    if bool(oracle.gap_reject()(inp.x, inp.Wr, inp.br, 3).any()):
+        pytest.skip("a token's routing is not unique under reassociation")
+    y, _ = _few(inp)
+    _close(y, _ref(inp))
 
 
 @pytest.mark.parametrize("wfmt", ["bf16", "mxfp4"])

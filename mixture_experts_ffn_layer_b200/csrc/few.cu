@@ -967,21 +967,27 @@ moe_status_t launch(FewParams p, cudaStream_t s) {
   const int red = kWarps * 128 * kN * 4;
   const int room = kMaxSmem - 4096 - p.T * p.row_pitch;
   if (mx) {
-    // as few parts of the reduction as let two stages fit
+    // as few parts of the reduction as let two stages fit where rows are copied
+    // as they lie, else four (a turn takes two) unless the pieces get shorter
+    // than 1 KB
     for (int which = 1; which <= 2; ++which) {
       const int units = (which == 1 ? p.D : p.I) / 32;
+      auto wanted = [&](int n) { return !mx_as_stored(units, n) && (units + n - 1) / n > 64 ? 4 : 2; };
       int nchunks = 1;
-      while (2 * mx_stage_bytes(units, nchunks) > room - red && nchunks < units) ++nchunks;
+      while (nchunks < units && wanted(nchunks) * mx_stage_bytes(units, nchunks) > room - red) ++nchunks;
       (which == 1 ? p.nchunks1 : p.nchunks2) = nchunks;
       p.slab_bytes = std::max(p.slab_bytes, mx_stage_bytes(units, nchunks));
     }
   }
   const int stage = mx ? p.slab_bytes : kWarps * kBfSlot;
-  // the partial sums' buffers after two stages, then as many stages as fit
-  p.red_bufs = kN == 1 && room - 4 * red >= 3 * stage ? 4 : room - 2 * red >= 2 * stage ? 2 : 1;
+  // the most buffers for the partial sums that leave three stages, else two
+  p.red_bufs = 0;
+  for (int least = 3; least >= 2 && p.red_bufs == 0; --least)
+    for (int bufs = kN == 1 ? 4 : 2; bufs >= 1 && p.red_bufs == 0; bufs /= 2)
+      if (room - bufs * red >= least * stage) p.red_bufs = bufs;
+  if (p.red_bufs == 0) return MOE_ERR_UNSUPPORTED;
   int stages = (room - p.red_bufs * red) / stage;
   if (stages > kMaxStages) stages = kMaxStages;
-  if (stages < 2) return MOE_ERR_UNSUPPORTED;
   p.stages = stages;
   const int smem = p.T * p.row_pitch + p.red_bufs * red + stages * stage;
   if (cudaFuncSetAttribute(few_kernel<kFmt, kN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)

@@ -76,6 +76,7 @@ constexpr int kMaxT = 16;
 constexpr int kMaxK = 8;
 constexpr int kMaxActive = kMaxT * kMaxK;
 constexpr int kMaxSmem = 232448;      // 227 KB per block
+constexpr int kStaticSmem = 4096;     // of it for FewShared
 constexpr int kMaxStages = 8;
 constexpr int kMaxBufs = 4;
 constexpr int64_t kMaxRowBytes = 65536 * 2;  // T * max(D, I) bf16 of resident activations
@@ -217,25 +218,6 @@ __device__ __forceinline__ void grid_exit(unsigned* header) {
   }
 }
 
-// Wait for a phase of an mbarrier, kBarrierNs at most. The clock is looked at
-// only now and then: reading it takes as long as these waits mostly last.
-__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity) {
-  uint64_t t0 = 0;
-  for (uint32_t i = 1; !sm100::mbar_try_wait(bar, parity); ++i) {
-    if ((i & 255u) == 0) {
-      const uint64_t now = sm100::globaltimer_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > kBarrierNs) return false;
-    }
-  }
-  return true;
-}
-
-// Wait inside the block for warps that are on their way.
-__device__ __forceinline__ void wait_local(uint32_t bar, uint32_t parity, unsigned* header) {
-  if (!wait_bounded(bar, parity)) record_status(reinterpret_cast<int*>(header), MOE_ERR_TIMEOUT);
-}
-
 // Order-preserving integer of a logit; NaN sorts below every number, -0 as +0.
 __device__ __forceinline__ uint32_t sort_key(float v) {
   if (!(v == v)) return 0u;
@@ -250,6 +232,7 @@ __device__ __forceinline__ float key_value(uint32_t key) {
 struct FewShared {
   uint64_t full[kMaxBufs], empty[kMaxBufs];        // of the partial-sum buffers
   uint64_t w_full[kMaxStages], w_empty[kMaxStages];  // of the MXFP4 ring
+  int gave_up;                   // a wait of this block ran out of time
   int n_active;
   uint32_t tokens[256];          // per expert: its tokens, a bit each
   uint8_t place[256];            // per expert: its place among the active ones
@@ -262,6 +245,32 @@ struct FewShared {
   uint32_t row_max[kMaxT];       // |largest| of each resident row (bf16 bits)
   float row_scale[kMaxT];        // what a resident row's sums are multiplied with
 };
+
+// Wait for a phase of an mbarrier, kBarrierNs at most, or until the block has
+// given up elsewhere. The clock is looked at only now and then: reading it takes
+// as long as these waits mostly last.
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, const volatile int* gave_up) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; !sm100::mbar_try_wait(bar, parity); ++i) {
+    if ((i & 255u) == 0) {
+      if (gave_up && *gave_up) return false;
+      const uint64_t now = sm100::globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kBarrierNs) return false;
+    }
+  }
+  return true;
+}
+
+// Wait inside the block for warps that are on their way.
+__device__ __forceinline__ void wait_local(uint32_t bar, uint32_t parity, FewShared& sh, unsigned* header) {
+  if (!wait_bounded(bar, parity, &sh.gave_up)) {
+    record_status(reinterpret_cast<int*>(header), MOE_ERR_TIMEOUT);
+    *static_cast<volatile int*>(&sh.gave_up) = 1;
+  }
+}
+
+static_assert(sizeof(FewShared) <= kStaticSmem, "");
 
 // One weight's granules as this block and warp see them.
 struct Stream {
@@ -405,7 +414,7 @@ __device__ __forceinline__ void mx_produce(const FewParams& p, FewShared& sh, co
       const uint8_t* w = (which == 1 ? p.w1 : p.w2) + row0 * st.row_bytes;
       const uint8_t* s = (which == 1 ? p.s1 : p.s2) + row0 * st.srow_bytes;
       for (int c = 0; c < st.nchunks; ++c) {
-        if (!idle && !wait_bounded(empty + 8 * slot, phase ^ 1u)) {
+        if (!idle && !wait_bounded(empty + 8 * slot, phase ^ 1u, &sh.gave_up)) {
           failed = true;
           break;
         }
@@ -445,13 +454,14 @@ __device__ __forceinline__ void mx_produce(const FewParams& p, FewShared& sh, co
   }
   if (failed) {
     if (lane == 0) record_status(reinterpret_cast<int*>(p.header), MOE_ERR_TIMEOUT);
+    *static_cast<volatile int*>(&sh.gave_up) = 1;
     // the copies still in flight land before the block can exit
     for (int i = min(issued, p.stages); i > 0; --i) {
       if (--slot < 0) {
         slot = p.stages - 1;
         phase ^= 1u;
       }
-      wait_bounded(full + 8 * slot, phase);
+      wait_bounded(full + 8 * slot, phase, nullptr);
     }
   }
 }
@@ -608,6 +618,7 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
   if (threadIdx.x < 256) sh.tokens[threadIdx.x] = 0;
   if (threadIdx.x < kMaxT) sh.row_max[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
+    sh.gave_up = 0;
     for (int i = 0; i < kMaxBufs; ++i) {
       sm100::mbar_init(sm100::smem_u32(&sh.full[i]), kWarps);
       sm100::mbar_init(sm100::smem_u32(&sh.empty[i]), kWarps);
@@ -827,7 +838,7 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
         const bool active = my_turn(turn);
         float sum[kTasks];
         if (active) {
-          wait_local(full_at + 8 * buf, (turn >> buf_shift) & 1, p.header);
+          wait_local(full_at + 8 * buf, (turn >> buf_shift) & 1, sh, p.header);
 #pragma unroll
           for (int i = 0; i < kTasks; ++i) {
             sum[i] = 0.0f;
@@ -882,7 +893,7 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
           // phase passes a warp by.
           const int count = min(s.turn, end - base);
           for (int i = 0; i < (count + 1) / 2 * s.nchunks; ++i) {
-            wait_local(sm100::smem_u32(&sh.w_full[slot]), slab_phase, p.header);
+            wait_local(sm100::smem_u32(&sh.w_full[slot]), slab_phase, sh, p.header);
             const int chunk = i - s.side / 2 * s.nchunks;
             if (chunk >= 0 && chunk < s.nchunks && s.side < count) {
               // this warp's units of the stage
@@ -919,7 +930,7 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
         // the warps' parts meet in buffer it mod red_bufs
         const int buf = it & (p.red_bufs - 1);
         float* part = red + buf * kRedFloats;
-        if (it >= p.red_bufs) wait_local(empty_at + 8 * buf, ((it >> buf_shift) - 1) & 1, p.header);
+        if (it >= p.red_bufs) wait_local(empty_at + 8 * buf, ((it >> buf_shift) - 1) & 1, sh, p.header);
 #pragma unroll
         for (int i = 0; i < kN; ++i)
           if (i == 0 || rows > 8)
@@ -965,7 +976,7 @@ template <int kFmt, int kN>
 moe_status_t launch(FewParams p, cudaStream_t s) {
   constexpr bool mx = kFmt == MOE_W_MXFP4;
   const int red = kWarps * 128 * kN * 4;
-  const int room = kMaxSmem - 4096 - p.T * p.row_pitch;
+  const int room = kMaxSmem - kStaticSmem - p.T * p.row_pitch;
   if (mx) {
     // as few parts of the reduction as let two stages fit where rows are copied
     // as they lie, else four (a turn takes two) unless the pieces get shorter
@@ -990,7 +1001,9 @@ moe_status_t launch(FewParams p, cudaStream_t s) {
   if (stages > kMaxStages) stages = kMaxStages;
   p.stages = stages;
   const int smem = p.T * p.row_pitch + p.red_bufs * red + stages * stage;
-  if (cudaFuncSetAttribute(few_kernel<kFmt, kN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  // (the same limit for every size: calls from several host threads do not meet another's)
+  if (cudaFuncSetAttribute(few_kernel<kFmt, kN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kMaxSmem - kStaticSmem) != cudaSuccess)
     return MOE_ERR_CUDA;
   void* args[] = {&p};
   if (cudaLaunchCooperativeKernel(reinterpret_cast<void*>(few_kernel<kFmt, kN>), dim3(num_sms()),

@@ -510,8 +510,9 @@ moe_status_t launch(Fp8Params p, const uint8_t* a, const uint8_t* w, cudaStream_
   p.stages = p.stages > kMaxStages ? kMaxStages : p.stages / 2 * 2;
   p.NT = (p.N + S_::kBN - 1) / S_::kBN;
   const size_t smem = fixed + p.stages * stage;
+  // (the same limit for every size: calls from several host threads do not meet another's)
   if (cudaFuncSetAttribute(fp8_gemm_kernel<S_>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess)
+                           static_cast<int>(kMaxSmem)) != cudaSuccess)
     return MOE_ERR_CUDA;
   const int64_t max_tiles = ((p.R + BM - 1) / BM + p.E) * static_cast<int64_t>(p.NT);
   const int grid = static_cast<int>(max_tiles < num_sms() ? max_tiles : num_sms());

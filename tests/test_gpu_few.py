@@ -241,3 +241,34 @@ def test_block_of_norm_and_layer(T, wfmt):
         assert float((y - ref).abs().max()) <= (2e-2 if wfmt == "bf16" else 6e-2) * float(ref.pow(2).mean().sqrt())
     want = layer.forward_few(n) if T == 2 else layer(n)
     assert torch.equal(y if T == 2 else y.to(BF16).cuda(), want)
+
+
+def test_two_host_threads():
+    # calls of different sizes from two threads at once, each with its own
+    # stream and workspace
+    import threading
+    cases = [_make(1, 512, 16, 4, 512, "mxfp4"), _make(7, 1024, 16, 4, 2048, "mxfp4")]
+    want = [_few(c) for c in cases]
+    torch.cuda.synchronize()
+    bad = []
+
+    def run(inp, y, ws):
+        try:
+            stream = torch.cuda.Stream()
+            out = torch.empty_like(y)
+            for _ in range(50):
+                _few(inp, ws=ws, y=out, stream=stream)
+            stream.synchronize()
+            if not torch.equal(out, y):
+                bad.append("differs")
+        except Exception as err:
+            bad.append(repr(err))
+
+    threads = [threading.Thread(target=run, args=(c, y, ws)) for c, (y, ws) in zip(cases, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert bad == []
+    for _, ws in want:
+        assert moe.moe_read_device_status(ws) == 0

@@ -272,6 +272,23 @@ __device__ __forceinline__ void wait_local(uint32_t bar, uint32_t parity, FewSha
 
 static_assert(sizeof(FewShared) <= kStaticSmem, "");
 
+// MXFP4: units per stage of a granule, even (K is a multiple of 64).
+__host__ __device__ constexpr int mx_chunk(int units, int nchunks) {
+  return ((units + nchunks - 1) / nchunks + 1) / 2 * 2;
+}
+// Bytes between a stage's rows of codes. Rows 32 or 96 bytes off a multiple of
+// 128 collide two ways at most and are copied as they lie, a granule's 8 or 16
+// at a time (a bulk copy costs its issuer some 60 ns whatever its size); others
+// are copied row by row to an odd multiple of 16 (no collision).
+__host__ __device__ constexpr bool mx_as_stored(int units, int nchunks) { return nchunks == 1 && units % 4 == 2; }
+__host__ __device__ constexpr int mx_pitch(int units, int nchunks, int chunk) {
+  return mx_as_stored(units, nchunks) ? units * 16 : (chunk | 1) * 16;
+}
+// A stage: 32 rows of codes, then all of the 32 rows' scales (with every chunk).
+__host__ __device__ constexpr int mx_stage_bytes(int units, int nchunks) {
+  return (32 * (mx_pitch(units, nchunks, mx_chunk(units, nchunks)) + units) + 127) / 128 * 128;
+}
+
 // One weight's granules as this block and warp see them.
 struct Stream {
   int64_t row_bytes;     // of the weight
@@ -311,7 +328,7 @@ __device__ __forceinline__ Stream make_stream(const FewParams& p, int which, int
   s.u0 = min(s.units, warp % split * per);
   s.u1 = min(s.units, s.u0 + per);
   s.nchunks = kFmt == MOE_W_BF16 ? (per + kBfUnits - 1) / kBfUnits : which == 1 ? p.nchunks1 : p.nchunks2;
-  s.chunk = (s.units + s.nchunks - 1) / s.nchunks;
+  s.chunk = mx_chunk(s.units, s.nchunks);
   return s;
 }
 
@@ -371,19 +388,6 @@ struct Loader {
     }
   }
 };
-
-// Bytes between a stage's rows of codes. Rows 32 or 96 bytes off a multiple of
-// 128 collide two ways at most and are copied as they lie, a granule's 8 or 16
-// at a time (a bulk copy costs its issuer some 60 ns whatever its size); others
-// are copied row by row to an odd multiple of 16 (no collision).
-__host__ __device__ constexpr bool mx_as_stored(int units, int nchunks) { return nchunks == 1 && units % 4 == 2; }
-__host__ __device__ constexpr int mx_pitch(int units, int nchunks, int chunk) {
-  return mx_as_stored(units, nchunks) ? units * 16 : (chunk | 1) * 16;
-}
-// A stage: 32 rows of codes, then all of the 32 rows' scales (with every chunk).
-__host__ __device__ constexpr int mx_stage_bytes(int units, int nchunks) {
-  return (32 * (mx_pitch(units, nchunks, (units + nchunks - 1) / nchunks) + units) + 127) / 128 * 128;
-}
 
 // The loading warps of an MXFP4 block: mlp1's granules then mlp2's, turn by
 // turn, two granules a stage. Of W1 rows 0..15 of a stage are gate rows and
@@ -488,36 +492,77 @@ __device__ __forceinline__ void mul_bf16(const uint8_t* slot, int r, int q, int 
   }
 }
 
-// The same for kUnits units of MXFP4 codes; at, at8: the lane's place in its
-// two rows of codes, s_lo, s_hi: in their scales. All four and b move on.
-template <int kG, int kUnits, int kN>
-__device__ __forceinline__ void mul_mx(const uint8_t*& at, const uint8_t*& at8, const uint8_t*& s_lo,
-                                       const uint8_t*& s_hi, const uint8_t* (&b)[kN], const float (&zero)[4],
-                                       float (&acc)[kN][4]) {
+// Four 8 x 16-byte matrices of shared memory, whose rows the lanes 8 m + i point
+// at: register m of lane 4 r + q holds bytes 4 q.. of row r of matrix m.
+__device__ __forceinline__ void ldmatrix_x4(uint32_t at, uint32_t (&v)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(at));
+}
+
+// The same for kUnits (even) units of MXFP4 codes, with the columns of an MMA's
+// activations shared by kPack units, 8 / kPack tokens each: one load of the
+// activations serves them all, and of each unit's sums a quarter of the lanes, or
+// a half, are its own -- those lanes bring its scale and add them (the others hold
+// products of one unit's codes with another's activations). at: the row of codes
+// that this lane points at for two units of the granule's first and last 8 rows;
+// s_lo, s_hi: the lane's place in its two rows' scales (of its own unit of the
+// kPack); own: which of them that is. All of them and b move on.
+template <int kG, int kUnits, int kPack, int kN>
+__device__ __forceinline__ void mul_mx(uint32_t& at, const uint8_t*& s_lo, const uint8_t*& s_hi,
+                                       const uint8_t* (&b)[kN], int own, const float (&zero)[4], float (&acc)[kN][4]) {
+  constexpr int kStep = kPack > 2 && kUnits > 2 ? 4 : 2;  // units that are begun together
 #pragma unroll
-  for (int j = 0; j < kUnits; ++j) {
-    uint32_t a[4], a8[4];
-    e2m1_to_f16(lds<uint32_t>(at + j * 16), a);
-    e2m1_to_f16(lds<uint32_t>(at8 + j * 16), a8);
-    const float w_lo = e8m0(lds<uint8_t>(s_lo + j)), w_hi = e8m0(lds<uint8_t>(s_hi + j));
+  for (int j = 0; j < kUnits; j += kStep) {
+    uint4 x[kG];
+    uint32_t w_lo, w_hi;
+    if (kPack == 1) {
+      w_lo = lds<uint16_t>(s_lo + j);
+      w_hi = lds<uint16_t>(s_hi + j);
+    } else {
+      w_lo = lds<uint8_t>(s_lo + j);
+      w_hi = lds<uint8_t>(s_hi + j);
 #pragma unroll
-    for (int g = 0; g < kG; ++g) {
-      const uint4 v = lds<uint4>(b[g] + j * 64);
-      float c[4];
-      mma_f16_16816_from(c, a[0], a8[0], a[1], a8[1], v.x, v.y, zero);
-      mma_f16_16816(c, a[2], a8[2], a[3], a8[3], v.z, v.w);
-      acc[g][0] = fmaf(w_lo, c[0], acc[g][0]);
-      acc[g][1] = fmaf(w_lo, c[1], acc[g][1]);
-      acc[g][2] = fmaf(w_hi, c[2], acc[g][2]);
-      acc[g][3] = fmaf(w_hi, c[3], acc[g][3]);
+      for (int g = 0; g < kG; ++g) x[g] = lds<uint4>(b[g] + j * 64);
+    }
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < kStep; ++i) {
+      if (i % 2 == 0) ldmatrix_x4(at + (j + i) * 16, v);
+      uint32_t a[4], a8[4];
+      e2m1_to_f16(v[i % 2], a);
+      e2m1_to_f16(v[2 + i % 2], a8);
+      const float f_lo = e8m0(kPack > 1 ? w_lo : i == 0 ? w_lo & 0xffu : w_lo >> 8);
+      const float f_hi = e8m0(kPack > 1 ? w_hi : i == 0 ? w_hi & 0xffu : w_hi >> 8);
+#pragma unroll
+      for (int g = 0; g < kG; ++g) {
+        if (kPack == 1) x[g] = lds<uint4>(b[g] + (j + i) * 64);
+        float c[4];
+        mma_f16_16816_from(c, a[0], a8[0], a[1], a8[1], x[g].x, x[g].y, zero);
+        mma_f16_16816(c, a[2], a8[2], a[3], a8[3], x[g].z, x[g].w);
+        if (kPack == 1 || own == i) {
+          acc[g][0] = fmaf(f_lo, c[0], acc[g][0]);
+          acc[g][1] = fmaf(f_lo, c[1], acc[g][1]);
+          acc[g][2] = fmaf(f_hi, c[2], acc[g][2]);
+          acc[g][3] = fmaf(f_hi, c[3], acc[g][3]);
+        }
+      }
     }
   }
   at += kUnits * 16;
-  at8 += kUnits * 16;
   s_lo += kUnits;
   s_hi += kUnits;
 #pragma unroll
   for (int g = 0; g < kG; ++g) b[g] += kUnits * 64;
+}
+// The same for `left` units, an even number, of one group of tokens.
+template <int kPack, int kN>
+__device__ __forceinline__ void mul_mx_row(int left, uint32_t at, const uint8_t* s_lo, const uint8_t* s_hi,
+                                           const uint8_t* (&b)[kN], int own, const float (&zero)[4],
+                                           float (&acc)[kN][4]) {
+  for (; left >= 8; left -= 8) mul_mx<1, 8, kPack>(at, s_lo, s_hi, b, own, zero, acc);
+  if (left & 4) mul_mx<1, 4, kPack>(at, s_lo, s_hi, b, own, zero, acc);
+  if (left & 2) mul_mx<1, 2, kPack>(at, s_lo, s_hi, b, own, zero, acc);
 }
 
 // Bring `rows` rows of K bf16 into shared memory; MXFP4 rows become f16
@@ -773,7 +818,7 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
     const Stream& s = which == 1 ? st1 : st2;
     if (which == 2) grid_barrier(p.header, kBar2);  // h is complete
     const int pitch = mx_pitch(s.units, s.nchunks, s.chunk);
-    const int split = kWarps / s.turn, tasks = s.turn * 4 * kN;
+    const int split = kWarps / s.turn;
     for (int ai = s.g0 / s.per_expert; s.g0 < s.g1 && ai * s.per_expert < s.g1; ++ai) {
       const int begin = max(0, s.g0 - ai * s.per_expert), end = min(s.per_expert, s.g1 - ai * s.per_expert);
       const int e = sh.expert[ai], start = sh.start[ai], rows = sh.start[ai + 1] - start;
@@ -784,17 +829,24 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
         load_rows<kFmt>(p, sh, p.h + static_cast<int64_t>(start) * p.I, rows, p.I, act);
         warps_sync();
       }
+      // MXFP4: up to 2 tokens share an MMA's columns with 4 units, up to 4 tokens
+      // with 2 (wide: log2 of the lanes of a row's four that a token's unit has; own:
+      // this lane's unit of the 4 or 2)
+      const int wide = kFmt == MOE_W_BF16 || rows > 4 ? 2 : rows > 2 ? 1 : 0, own = fq >> wide;
       // a column without a token repeats the last row; its sums are not used
       const uint8_t* brow[kN];
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
-        const int n = min(8 * i + fr, rows - 1);
-        brow[i] = act + (which == 1 ? nth_bit(sh.tokens[e], n) : n) * p.row_pitch + (kFmt == MOE_W_BF16 ? s.u0 * 64 : 0) + fq * 16;
+        const int n = min(8 * i + (fr & ((2 << wide) - 1)), rows - 1);
+        brow[i] = act + (which == 1 ? nth_bit(sh.tokens[e], n) : n) * p.row_pitch + fq * 16 +
+                  (kFmt == MOE_W_BF16 ? s.u0 * 64 : (fr >> (wide + 1)) * 64);
       }
-      // A turn's granules are finished by `tasks` warps' worth of work, 128 sums
-      // each; a warp always has the same tasks (every turn, or every second or
-      // fourth where there are fewer tasks than warps), so what they need is
-      // worked out once for the expert.
+      // A turn's granules are finished by `tasks` warps' worth of work, 32 sums
+      // each: of a fragment's 128, those of the first unit of the 4 or 2, to which
+      // the others' are added. A warp always has the same tasks (every turn, or every
+      // second, fourth, ... where there are fewer tasks than warps), so what they
+      // need is worked out once for the expert.
+      const int groups = kFmt == MOE_W_MXFP4 && rows <= 8 ? 1 : kN, tasks = (s.turn * groups) << wide;
       constexpr int kTasks = kN;  // at most, of a warp
       struct Task {
         bool mine, on;       // there is one, of a group with tokens; this lane's sum is of one of them
@@ -808,11 +860,13 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
 #pragma unroll
       for (int i = 0; i < kTasks; ++i) {
         const int id = (warp & (tasks - 1)) + kWarps * i;
-        const int grp = id / 4 % kN, at = (id % 4) * 32 + lane;
+        const int grp = (id >> wide) & (groups - 1);
         // fragment element -> weight row r and token n
+        const int el = (id & ((1 << wide) - 1)) * 32 + lane, frag = el / 4;
+        const int at = ((frag >> wide) * 4 + (frag & ((1 << wide) - 1))) * 4 + el % 4;
         const int r = at / 16 + (at & 2 ? 8 : 0), n = 8 * grp + (at / 4 % 4) * 2 + (at & 1);
         task[i].mine = id < tasks && 8 * grp < rows;
-        task[i].m = id / (4 * kN);
+        task[i].m = (id >> wide) / groups;
         task[i].on = task[i].mine && n < rows;
         const int row = start + (n < rows ? n : 0), a = sh.slot[row];
         task[i].part = red + (task[i].m * split * kN + grp) * 128 + at;
@@ -844,8 +898,10 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
             sum[i] = 0.0f;
             if (task[i].mine) {
               const float* part = task[i].part + buf * kRedFloats;
+              for (int c = 0; c < 16; c += 4 << wide) {
 #pragma unroll 4
-              for (int w = 0; w < split; ++w) sum[i] += part[w * (kN * 128)];
+                for (int w = 0; w < split; ++w) sum[i] += part[w * (kN * 128) + c];
+              }
             }
           }
           __syncwarp();
@@ -896,27 +952,30 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
             wait_local(sm100::smem_u32(&sh.w_full[slot]), slab_phase, sh, p.header);
             const int chunk = i - s.side / 2 * s.nchunks;
             if (chunk >= 0 && chunk < s.nchunks && s.side < count) {
-              // this warp's units of the stage
-              const int first = chunk * s.chunk, n = min(s.chunk, s.units - first), per = (n + split - 1) / split;
+              // this warp's units of the stage, an even number
+              const int first = chunk * s.chunk, n = min(s.chunk, s.units - first), per = (n + 2 * split - 1) / (2 * split) * 2;
               const int u0 = min(n, warp % split * per);
               int left = min(n, u0 + per) - u0;
               const uint8_t* slab = ring + slot * p.slab_bytes;
-              const int lo = (which == 1 ? 8 : 16) * (s.side & 1) + fr, hi = lo + (which == 1 ? 16 : 8);  // its rows
-              const uint8_t* at = slab + lo * pitch + u0 * 16 + fq * 4;
-              const uint8_t* at8 = at + (hi - lo) * pitch;
-              const uint8_t* s_lo = slab + 32 * pitch + lo * s.srow_bytes + first + u0;
+              const int lo = (which == 1 ? 8 : 16) * (s.side & 1), hi = lo + (which == 1 ? 16 : 8);  // its rows
+              // codes: lanes 0..7 and 8..15 point at the first 8 rows, at one unit
+              // and the next, 16..31 at the last 8
+              uint32_t at = sm100::smem_u32(slab) + ((lane & 16 ? hi : lo) + (lane & 7)) * pitch +
+                            (u0 + ((lane >> 3) & 1)) * 16;
+              const uint8_t* s_lo = slab + 32 * pitch + (lo + fr) * s.srow_bytes + first + u0 + own;
               const uint8_t* s_hi = s_lo + (hi - lo) * s.srow_bytes;
               const uint8_t* b[kN];
 #pragma unroll
               for (int j = 0; j < kN; ++j) b[j] = brow[j] + (first + u0) * 64;
-              if (kN == 1 || rows <= 8) {
-                for (; left >= 8; left -= 8) mul_mx<1, 8>(at, at8, s_lo, s_hi, b, zero, acc);
-                if (left & 4) mul_mx<1, 4>(at, at8, s_lo, s_hi, b, zero, acc);
-                if (left & 2) mul_mx<1, 2>(at, at8, s_lo, s_hi, b, zero, acc);
-                if (left & 1) mul_mx<1, 1>(at, at8, s_lo, s_hi, b, zero, acc);
+              if (wide == 0) {
+                mul_mx_row<4>(left, at, s_lo, s_hi, b, own, zero, acc);
+              } else if (wide == 1) {
+                mul_mx_row<2>(left, at, s_lo, s_hi, b, own, zero, acc);
+              } else if (kN == 1 || rows <= 8) {
+                mul_mx_row<1>(left, at, s_lo, s_hi, b, own, zero, acc);
               } else {
-                for (; left >= 4; left -= 4) mul_mx<kN, 4>(at, at8, s_lo, s_hi, b, zero, acc);
-                for (; left > 0; --left) mul_mx<kN, 1>(at, at8, s_lo, s_hi, b, zero, acc);
+                for (; left >= 4; left -= 4) mul_mx<kN, 4, 1>(at, s_lo, s_hi, b, own, zero, acc);
+                if (left) mul_mx<kN, 2, 1>(at, s_lo, s_hi, b, own, zero, acc);
               }
             }
             __syncwarp();
@@ -976,7 +1035,9 @@ template <int kFmt, int kN>
 moe_status_t launch(FewParams p, cudaStream_t s) {
   constexpr bool mx = kFmt == MOE_W_MXFP4;
   const int red = kWarps * 128 * kN * 4;
-  const int room = kMaxSmem - kStaticSmem - p.T * p.row_pitch;
+  // (lanes whose unit of a shared MMA lies past the last one read up to 3 bytes past the last stage's scales)
+  constexpr int past = 16;
+  const int room = kMaxSmem - kStaticSmem - past - p.T * p.row_pitch;
   if (mx) {
     // as few parts of the reduction as let two stages fit where rows are copied
     // as they lie, else four (a turn takes two) unless the pieces get shorter
@@ -986,6 +1047,7 @@ moe_status_t launch(FewParams p, cudaStream_t s) {
       auto wanted = [&](int n) { return !mx_as_stored(units, n) && (units + n - 1) / n > 64 ? 4 : 2; };
       int nchunks = 1;
       while (nchunks < units && wanted(nchunks) * mx_stage_bytes(units, nchunks) > room - red) ++nchunks;
+      nchunks = (units + mx_chunk(units, nchunks) - 1) / mx_chunk(units, nchunks);
       (which == 1 ? p.nchunks1 : p.nchunks2) = nchunks;
       p.slab_bytes = std::max(p.slab_bytes, mx_stage_bytes(units, nchunks));
     }
@@ -1000,7 +1062,7 @@ moe_status_t launch(FewParams p, cudaStream_t s) {
   int stages = (room - p.red_bufs * red) / stage;
   if (stages > kMaxStages) stages = kMaxStages;
   p.stages = stages;
-  const int smem = p.T * p.row_pitch + p.red_bufs * red + stages * stage;
+  const int smem = p.T * p.row_pitch + p.red_bufs * red + stages * stage + past;
   // (the same limit for every size: calls from several host threads do not meet another's)
   if (cudaFuncSetAttribute(few_kernel<kFmt, kN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            kMaxSmem - kStaticSmem) != cudaSuccess)

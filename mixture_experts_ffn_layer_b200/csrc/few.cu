@@ -240,7 +240,8 @@ struct FewShared {
   uint8_t start[kMaxActive + 1]; // first row of each active expert
   uint8_t slot[kMaxActive];      // per row: its assignment t * k + j
   uint8_t top[kMaxT][kMaxK];     // expert of each assignment
-  float gate[kMaxT][kMaxK];
+  uint8_t token[kMaxActive];     // per row
+  float gate[kMaxActive];        // per assignment
   float dot[kWarps];
   uint32_t row_max[kMaxT];       // |largest| of each resident row (bf16 bits)
   float row_scale[kMaxT];        // what a resident row's sums are multiplied with
@@ -298,7 +299,8 @@ struct Stream {
   int step;              // weight rows a granule advances by (8 or 16)
   int per_expert;        // granules per expert
   int turn;              // granules that the block works on at a time, kWarps / turn warps on each
-  int side;              // this warp's granule of them
+  int split_log2;        // log2 of those warps
+  int side, part;        // this warp's granule of them, its part of the granule's reduction
   int u0, u1;            // this warp's units of 32 of the reduction
   int units;             // units of the reduction
   int nchunks;           // stages per granule
@@ -320,12 +322,13 @@ __device__ __forceinline__ Stream make_stream(const FewParams& p, int which, int
   const uint32_t n = n_active * s.per_expert;  // at most 128 * 2048
   s.g0 = static_cast<int>(n * blockIdx.x / gridDim.x);
   s.g1 = static_cast<int>(n * (blockIdx.x + 1) / gridDim.x);
-  s.turn = kFmt == MOE_W_BF16 ? 1 : n / gridDim.x >= 4 ? 4 : 2;
-  const int split = kWarps / s.turn;
-  s.side = warp / split;
+  s.split_log2 = kFmt == MOE_W_BF16 ? 4 : n >= 4 * gridDim.x ? 2 : 3;
+  s.turn = kWarps >> s.split_log2;
+  s.side = warp >> s.split_log2;
+  s.part = warp & ((1 << s.split_log2) - 1);
   // bf16: this warp's units, two a stage
-  const int per = (s.units + split - 1) / split;
-  s.u0 = min(s.units, warp % split * per);
+  const int per = (s.units + (1 << s.split_log2) - 1) >> s.split_log2;
+  s.u0 = min(s.units, s.part * per);
   s.u1 = min(s.units, s.u0 + per);
   s.nchunks = kFmt == MOE_W_BF16 ? (per + kBfUnits - 1) / kBfUnits : which == 1 ? p.nchunks1 : p.nchunks2;
   s.chunk = mx_chunk(s.units, s.nchunks);
@@ -567,25 +570,29 @@ __device__ __forceinline__ void mul_mx_row(int left, uint32_t at, const uint8_t*
 
 // Bring `rows` rows of K bf16 into shared memory; MXFP4 rows become f16
 // scaled by a power of two. row_max is zero on entry, and the warps
-// synchronise before they read the rows.
-template <int kFmt>
+// synchronise before they read the rows. kHere: the rows are in shared memory
+// already, where each thread has copied the pieces that it handles here.
+template <int kFmt, bool kHere>
 __device__ __forceinline__ void load_rows(const FewParams& p, FewShared& sh, const uint16_t* from, int rows, int K,
                                           uint8_t* act) {
   const int per = K / 8;  // 16-byte chunks per row
   constexpr int kAtOnce = 4;  // rows in flight
   for (int n0 = 0; n0 < rows; n0 += kAtOnce) {
+    if (kHere && kFmt == MOE_W_BF16) break;
     for (int base = threadIdx.x & ~31; base < per; base += kThreads) {  // (uniform in a warp)
       const int c = base + (threadIdx.x & 31);
       uint4 v[kAtOnce];
 #pragma unroll
-      for (int z = 0; z < kAtOnce; ++z)
-        v[z] = n0 + z < rows && c < per
-                   ? __ldcg(reinterpret_cast<const uint4*>(from) + static_cast<int64_t>(n0 + z) * per + c)
-                   : make_uint4(0, 0, 0, 0);
+      for (int z = 0; z < kAtOnce; ++z) {
+        v[z] = make_uint4(0, 0, 0, 0);
+        if (n0 + z < rows && c < per)
+          v[z] = kHere ? lds<uint4>(act + (n0 + z) * p.row_pitch + c * 16)
+                       : __ldcg(reinterpret_cast<const uint4*>(from) + static_cast<int64_t>(n0 + z) * per + c);
+      }
 #pragma unroll
       for (int z = 0; z < kAtOnce; ++z) {
         if (n0 + z >= rows) break;
-        if (c < per) *reinterpret_cast<uint4*>(act + (n0 + z) * p.row_pitch + c * 16) = v[z];
+        if (!kHere && c < per) *reinterpret_cast<uint4*>(act + (n0 + z) * p.row_pitch + c * 16) = v[z];
         if (kFmt == MOE_W_MXFP4) {
           const uint32_t w[4] = {v[z].x, v[z].y, v[z].z, v[z].w};
           uint32_t m = 0;
@@ -599,35 +606,41 @@ __device__ __forceinline__ void load_rows(const FewParams& p, FewShared& sh, con
   }
   if (kFmt == MOE_W_MXFP4) {
     warps_sync();
-    for (int n = 0; n < rows; ++n) {
-      // 2^shift brings the row's largest magnitude into [2^8, 2^9); a row of
-      // zeros, or with an infinity or NaN, stays as it is
-      const uint32_t largest = sh.row_max[n];
-      const int ex = static_cast<int>(largest >> 7);  // biased exponent
-      const int shift = largest == 0 || ex == 255 ? 0 : min(127, 8 + 127 - max(ex, 1));
-      const float mul = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
-      if (threadIdx.x == 0)
-        sh.row_scale[n] = __uint_as_float(shift == 127 ? 0x00400000u : static_cast<uint32_t>(127 - shift) << 23);
-      for (int c = threadIdx.x; c < per; c += kThreads) {
-        uint4* at = reinterpret_cast<uint4*>(act + n * p.row_pitch + c * 16);
-        const uint4 v = *at;
-        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    for (int n0 = 0; n0 < rows; n0 += kAtOnce) {
+      float mul[kAtOnce];
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          const __half2 h2 = __floats2half2_rn(__uint_as_float(w[z] << 16) * mul,
-                                               __uint_as_float(w[z] & 0xffff0000u) * mul);
-          w[z] = *reinterpret_cast<const uint32_t*>(&h2);
+      for (int z = 0; z < kAtOnce; ++z) {
+        // 2^shift brings the row's largest magnitude into [2^8, 2^9); a row of
+        // zeros, or with an infinity or NaN, stays as it is
+        const int n = min(n0 + z, rows - 1);
+        const uint32_t largest = sh.row_max[n];
+        const int ex = static_cast<int>(largest >> 7);  // biased exponent
+        const int shift = largest == 0 || ex == 255 ? 0 : min(127, 8 + 127 - max(ex, 1));
+        mul[z] = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
+        if (threadIdx.x == 0)
+          sh.row_scale[n] = __uint_as_float(shift == 127 ? 0x00400000u : static_cast<uint32_t>(127 - shift) << 23);
+      }
+      for (int c = threadIdx.x; c < per; c += kThreads) {
+        uint8_t* at = act + n0 * p.row_pitch + c * 16;
+        uint4 v[kAtOnce];
+#pragma unroll
+        for (int z = 0; z < kAtOnce; ++z)
+          if (n0 + z < rows) v[z] = lds<uint4>(at + z * p.row_pitch);
+#pragma unroll
+        for (int z = 0; z < kAtOnce; ++z) {
+          if (n0 + z >= rows) break;
+          uint32_t w[4] = {v[z].x, v[z].y, v[z].z, v[z].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const __half2 h2 = __floats2half2_rn(__uint_as_float(w[i] << 16) * mul[z],
+                                                 __uint_as_float(w[i] & 0xffff0000u) * mul[z]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h2);
+          }
+          *reinterpret_cast<uint4*>(at + z * p.row_pitch) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        *at = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
   }
-}
-
-// The n-th set bit of a mask (n below its number of bits).
-__device__ __forceinline__ int nth_bit(uint32_t mask, int n) {
-  for (; n > 0; --n) mask &= mask - 1;
-  return __ffs(mask) - 1;
 }
 
 template <int kFmt, int kN>
@@ -659,7 +672,12 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
     }
   }
 
-  // ---- router logits; the tokens' rows
+  // ---- the tokens' rows are asked for (by the threads that look at them below);
+  // router logits
+  for (int n = 0; n < p.T; ++n)
+    for (int c = threadIdx.x; c < p.D / 8; c += kThreads)
+      cp_async16(sm100::smem_u32(act + n * p.row_pitch + c * 16), p.x + static_cast<int64_t>(n) * p.D + c * 8);
+  cp_commit();
   if (threadIdx.x < 256) sh.tokens[threadIdx.x] = 0;
   if (threadIdx.x < kMaxT) sh.row_max[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
@@ -679,26 +697,42 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
     int groups = 1;
     while (groups < n && groups < kWarps) groups *= 2;
     const int parts = kWarps / groups, part = warp % parts;
-    for (int i = warp / parts; i < n; i += groups) {
-      const int t = (i0 + i) / p.E, e = (i0 + i) % p.E;
-      const uint4* xr = reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(t) * p.D);
-      const uint4* wr = reinterpret_cast<const uint4*>(p.Wr + static_cast<int64_t>(e) * p.D);
-      float sum = 0.0f;
-#pragma unroll 6
-      for (int c = part * 32 + lane; c < p.D / 8; c += parts * 32) {
-        const uint4 a = __ldg(xr + c), b = __ldg(wr + c);
-        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+    // the first weights are on their way while the tokens' rows arrive
+    constexpr int kAhead = 6;
+    const int step = parts * 32, c0 = part * 32 + lane;
+    uint4 b[kAhead];
+    auto ask = [&](int i, int c) {
+      const uint4* from = reinterpret_cast<const uint4*>(p.Wr + static_cast<int64_t>((i0 + i) % p.E) * p.D);
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          sum = fmaf(__uint_as_float(aw[z] << 16), __uint_as_float(bw[z] << 16), sum);
-          sum = fmaf(__uint_as_float(aw[z] & 0xffff0000u), __uint_as_float(bw[z] & 0xffff0000u), sum);
+      for (int z = 0; z < kAhead; ++z)
+        if (c + z * step < p.D / 8) b[z] = __ldg(from + c + z * step);
+    };
+    int i = warp / parts;
+    if (i < n) ask(i, c0);
+    cp_wait<0>();
+    warps_sync();
+    for (bool asked = true; i < n; i += groups, asked = false) {
+      const uint8_t* row = act + (i0 + i) / p.E * p.row_pitch;
+      float sum = 0.0f;
+      for (int c = c0; c < p.D / 8; c += kAhead * step) {
+        if (!asked || c > c0) ask(i, c);
+#pragma unroll
+        for (int z = 0; z < kAhead; ++z) {
+          if (c + z * step >= p.D / 8) break;
+          const uint4 a = lds<uint4>(row + (c + z * step) * 16);
+          const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b[z].x, b[z].y, b[z].z, b[z].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            sum = fmaf(__uint_as_float(aw[j] << 16), __uint_as_float(bw[j] << 16), sum);
+            sum = fmaf(__uint_as_float(aw[j] & 0xffff0000u), __uint_as_float(bw[j] & 0xffff0000u), sum);
+          }
         }
       }
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
       if (lane == 0) {
         if (parts == 1)
-          p.logits[i0 + i] = sum + bf16_bits_to_float(p.br[e]);
+          p.logits[i0 + i] = sum + bf16_bits_to_float(p.br[(i0 + i) % p.E]);
         else
           sh.dot[warp] = sum;
       }
@@ -711,7 +745,7 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
       p.logits[at] = sum + bf16_bits_to_float(p.br[at % p.E]);
     }
   }
-  load_rows<kFmt>(p, sh, p.x, p.T, p.D, act);
+  load_rows<kFmt, true>(p, sh, p.x, p.T, p.D, act);
   grid_barrier(p.header, kBar1);
 
   // ---- top-k of every token (warp t), then the active experts
@@ -728,12 +762,12 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
       uint32_t best = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (!((taken >> i) & 1u)) best = max(best, key[i]);
+        if (32 * i < p.E && !((taken >> i) & 1u)) best = max(best, key[i]);
       best = __reduce_max_sync(0xffffffffu, best);
       uint32_t at = 0xffffffffu;  // lowest expert that holds it and is not taken
 #pragma unroll
       for (int i = 7; i >= 0; --i)
-        if (!((taken >> i) & 1u) && key[i] == best && lane + 32 * i < p.E) at = lane + 32 * i;
+        if (32 * i < p.E && !((taken >> i) & 1u) && key[i] == best && lane + 32 * i < p.E) at = lane + 32 * i;
       at = __reduce_min_sync(0xffffffffu, at);
       if (static_cast<int>(at & 31u) == lane) taken |= 1u << (at >> 5);
       const float v = key_value(best);
@@ -746,31 +780,36 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
         atomicOr(&sh.tokens[at], 1u << warp);
       }
     }
-    if (lane < p.k) sh.gate[warp][lane] = __fdividef(mine, total);
+    if (lane < p.k) sh.gate[warp * p.k + lane] = __fdividef(mine, total);
   }
   warps_sync();
   if (warp == 0) {
-    int n = 0, rows = 0;  // active experts and rows before expert 32 i
-    for (int base = 0; base < p.E; base += 32) {
-      const int e = base + lane;
-      const int mine = __popc(sh.tokens[e]);
-      int incl = mine;
+    // experts 8 lane .. 8 lane + 7; active experts and rows before them
+    uint32_t mask[8];
+    int n = 0, rows = 0;
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += v;
-      }
-      const uint32_t has = __ballot_sync(0xffffffffu, mine != 0);
-      if (mine) {
-        const int at = n + __popc(has & ((1u << lane) - 1u));
-        sh.place[e] = static_cast<uint8_t>(at);
-        sh.expert[at] = static_cast<uint8_t>(e);
-        sh.start[at] = static_cast<uint8_t>(rows + incl - mine);
-      }
-      n += __popc(has);
-      rows += __shfl_sync(0xffffffffu, incl, 31);
+    for (int i = 0; i < 8; ++i) {
+      mask[i] = sh.tokens[8 * lane + i];
+      n += mask[i] != 0;
+      rows += __popc(mask[i]);
     }
-    if (lane == 0) {
+    int both = n << 16 | rows;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, both, off);
+      if (lane >= off) both += v;
+    }
+    n = (both >> 16) - n;
+    rows = (both & 0xffff) - rows;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (mask[i] == 0) continue;
+      sh.place[8 * lane + i] = static_cast<uint8_t>(n);
+      sh.expert[n] = static_cast<uint8_t>(8 * lane + i);
+      sh.start[n++] = static_cast<uint8_t>(rows);
+      rows += __popc(mask[i]);
+    }
+    if (lane == 31) {
       sh.n_active = n;
       sh.start[n] = static_cast<uint8_t>(rows);
     }
@@ -778,7 +817,9 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
   warps_sync();
   if (static_cast<int>(threadIdx.x) < p.T * p.k) {
     const int t = threadIdx.x / p.k, e = sh.top[t][threadIdx.x % p.k];
-    sh.slot[sh.start[sh.place[e]] + __popc(sh.tokens[e] & ((1u << t) - 1u))] = static_cast<uint8_t>(threadIdx.x);
+    const int row = sh.start[sh.place[e]] + __popc(sh.tokens[e] & ((1u << t) - 1u));
+    sh.slot[row] = static_cast<uint8_t>(threadIdx.x);
+    sh.token[row] = static_cast<uint8_t>(t);
   }
   const int n_active = sh.n_active;
 
@@ -818,7 +859,6 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
     const Stream& s = which == 1 ? st1 : st2;
     if (which == 2) grid_barrier(p.header, kBar2);  // h is complete
     const int pitch = mx_pitch(s.units, s.nchunks, s.chunk);
-    const int split = kWarps / s.turn;
     for (int ai = s.g0 / s.per_expert; s.g0 < s.g1 && ai * s.per_expert < s.g1; ++ai) {
       const int begin = max(0, s.g0 - ai * s.per_expert), end = min(s.per_expert, s.g1 - ai * s.per_expert);
       const int e = sh.expert[ai], start = sh.start[ai], rows = sh.start[ai + 1] - start;
@@ -826,7 +866,7 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
         warps_sync();  // the previous expert's rows are read no more
         if (threadIdx.x < kMaxT) sh.row_max[threadIdx.x] = 0;
         warps_sync();
-        load_rows<kFmt>(p, sh, p.h + static_cast<int64_t>(start) * p.I, rows, p.I, act);
+        load_rows<kFmt, false>(p, sh, p.h + static_cast<int64_t>(start) * p.I, rows, p.I, act);
         warps_sync();
       }
       // MXFP4: up to 2 tokens share an MMA's columns with 4 units, up to 4 tokens
@@ -838,7 +878,7 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
         const int n = min(8 * i + (fr & ((2 << wide) - 1)), rows - 1);
-        brow[i] = act + (which == 1 ? nth_bit(sh.tokens[e], n) : n) * p.row_pitch + fq * 16 +
+        brow[i] = act + (which == 1 ? sh.token[start + n] : n) * p.row_pitch + fq * 16 +
                   (kFmt == MOE_W_BF16 ? s.u0 * 64 : (fr >> (wide + 1)) * 64);
       }
       // A turn's granules are finished by `tasks` warps' worth of work, 32 sums
@@ -846,7 +886,9 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
       // the others' are added. A warp always has the same tasks (every turn, or every
       // second, fourth, ... where there are fewer tasks than warps), so what they
       // need is worked out once for the expert.
-      const int groups = kFmt == MOE_W_MXFP4 && rows <= 8 ? 1 : kN, tasks = (s.turn * groups) << wide;
+      const int groups_log2 = kN == 1 || (kFmt == MOE_W_MXFP4 && rows <= 8) ? 0 : 1;
+      const int tasks_log2 = 4 - s.split_log2 + groups_log2 + wide, tasks = 1 << tasks_log2;
+      const int turns_mask = tasks < kWarps ? (kWarps >> tasks_log2) - 1 : 0, my_turn = (warp >> tasks_log2) & turns_mask;
       constexpr int kTasks = kN;  // at most, of a warp
       struct Task {
         bool mine, on;       // there is one, of a group with tokens; this lane's sum is of one of them
@@ -860,27 +902,26 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
 #pragma unroll
       for (int i = 0; i < kTasks; ++i) {
         const int id = (warp & (tasks - 1)) + kWarps * i;
-        const int grp = (id >> wide) & (groups - 1);
+        const int grp = (id >> wide) & ((1 << groups_log2) - 1);
         // fragment element -> weight row r and token n
         const int el = (id & ((1 << wide) - 1)) * 32 + lane, frag = el / 4;
         const int at = ((frag >> wide) * 4 + (frag & ((1 << wide) - 1))) * 4 + el % 4;
         const int r = at / 16 + (at & 2 ? 8 : 0), n = 8 * grp + (at / 4 % 4) * 2 + (at & 1);
         task[i].mine = id < tasks && 8 * grp < rows;
-        task[i].m = (id >> wide) / groups;
+        task[i].m = id >> (wide + groups_log2);
         task[i].on = task[i].mine && n < rows;
         const int row = start + (n < rows ? n : 0), a = sh.slot[row];
-        task[i].part = red + (task[i].m * split * kN + grp) * 128 + at;
-        task[i].scale = kFmt == MOE_W_BF16 ? 1.0f : sh.row_scale[which == 1 ? a / p.k : row - start];
-        task[i].gate = sh.gate[a / p.k][a % p.k];
+        task[i].part = red + ((task[i].m << s.split_log2) * kN + grp) * 128 + at;
+        task[i].scale = kFmt == MOE_W_BF16 ? 1.0f : sh.row_scale[which == 1 ? sh.token[row] : row - start];
+        task[i].gate = sh.gate[a];
         task[i].bias = which == 1 ? p.b1 + static_cast<int64_t>(e) * 2 * p.I + (r < 8 ? r : p.I + r - 8)
                                   : p.b2 + static_cast<int64_t>(e) * p.D + r;
         task[i].out = which == 1 ? static_cast<int64_t>(row) * p.I + r : static_cast<int64_t>(a) * p.D + r;
         if (which == 1 && r >= 8) task[i].on = false;  // an up half: its gate's lane writes h
       }
-      auto my_turn = [&](int turn) { return tasks >= kWarps || warp / tasks == (turn & (kWarps / tasks - 1)); };
       // What the finish needs from memory, asked for a turn ahead.
       auto load_bias = [&](int first, int turn) {
-        if (!my_turn(turn)) return;
+        if ((turn & turns_mask) != my_turn) return;
 #pragma unroll
         for (int i = 0; i < kTasks; ++i) {
           const int local = first + task[i].m;
@@ -889,7 +930,7 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
       };
       auto finish = [&](int first, int turn) {
         const int buf = turn & (p.red_bufs - 1);
-        const bool active = my_turn(turn);
+        const bool active = (turn & turns_mask) == my_turn;
         float sum[kTasks];
         if (active) {
           wait_local(full_at + 8 * buf, (turn >> buf_shift) & 1, sh, p.header);
@@ -900,7 +941,7 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
               const float* part = task[i].part + buf * kRedFloats;
               for (int c = 0; c < 16; c += 4 << wide) {
 #pragma unroll 4
-                for (int w = 0; w < split; ++w) sum[i] += part[w * (kN * 128) + c];
+                for (int w = 0; w < 1 << s.split_log2; ++w) sum[i] += part[w * (kN * 128) + c];
               }
             }
           }
@@ -953,8 +994,8 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
             const int chunk = i - s.side / 2 * s.nchunks;
             if (chunk >= 0 && chunk < s.nchunks && s.side < count) {
               // this warp's units of the stage, an even number
-              const int first = chunk * s.chunk, n = min(s.chunk, s.units - first), per = (n + 2 * split - 1) / (2 * split) * 2;
-              const int u0 = min(n, warp % split * per);
+              const int first = chunk * s.chunk, n = min(s.chunk, s.units - first), per = (n + (2 << s.split_log2) - 1) >> (s.split_log2 + 1) << 1;
+              const int u0 = min(n, s.part * per);
               int left = min(n, u0 + per) - u0;
               const uint8_t* slab = ring + slot * p.slab_bytes;
               const int lo = (which == 1 ? 8 : 16) * (s.side & 1), hi = lo + (which == 1 ? 16 : 8);  // its rows

@@ -72,6 +72,11 @@ namespace {
 constexpr int kWarps = 16;             // that compute
 constexpr int kLoaders = 4;            // that load, in an MXFP4 block
 constexpr int kThreads = kWarps * 32;
+// Registers per thread of an MXFP4 block's loading and computing warps, out of
+// the 96 that 640 threads are launched with.
+constexpr int kRegsLaunch = 65536 / (kThreads + 32 * kLoaders) / 8 * 8, kRegsLoad = 32;
+constexpr int kRegsCompute = (kRegsLaunch * (kThreads + 32 * kLoaders) - kRegsLoad * 32 * kLoaders) / kThreads / 8 * 8;
+static_assert(kLoaders == 4 && kRegsCompute > kRegsLaunch, "");
 constexpr int kMaxT = 16;
 constexpr int kMaxK = 8;
 constexpr int kMaxActive = kMaxT * kMaxK;
@@ -438,8 +443,8 @@ __device__ __forceinline__ void mx_produce(const FewParams& p, FewShared& sh, co
         } else {
           const int i = lane * kLoaders + loader, r = i % run;  // the lane's row, of the first 8 lanes
           if (i < runs * run)
-            bulk_load(to + (i / run * 16 + r) * pitch, w + (r + i / run * st.up) * st.row_bytes + c * st.chunk * 16, n * 16,
-                      bar);
+            bulk_load(to + (i / run * 16 + r) * pitch, w + (r + i / run * st.up) * st.row_bytes + c * st.chunk * 16,
+                      n * 16, bar);
         }
         ++issued;
         if (++slot == p.stages) {
@@ -644,7 +649,8 @@ __device__ __forceinline__ void load_rows(const FewParams& p, FewShared& sh, con
 }
 
 template <int kFmt, int kN>
-__global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoaders : 0), 1) few_kernel(const FewParams p) {
+__global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoaders : 0), 1)
+    few_kernel(const FewParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   // resident rows | partial sums | rings
   uint8_t* act = smem;
@@ -665,11 +671,13 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
       sm100::fence_mbar_init();
     }
     if (warp >= kWarps) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLoad));
       __syncthreads();  // the lists are complete
       mx_produce(p, sh, make_stream<kFmt>(p, 1, sh.n_active, 0), make_stream<kFmt>(p, 2, sh.n_active, 0),
                  sm100::smem_u32(ring), warp - kWarps, lane);
       return;
     }
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsCompute));
   }
 
   // ---- the tokens' rows are asked for (by the threads that look at them below);
@@ -881,84 +889,117 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
         brow[i] = act + (which == 1 ? sh.token[start + n] : n) * p.row_pitch + fq * 16 +
                   (kFmt == MOE_W_BF16 ? s.u0 * 64 : (fr >> (wide + 1)) * 64);
       }
-      // A turn's granules are finished by `tasks` warps' worth of work, 32 sums
-      // each: of a fragment's 128, those of the first unit of the 4 or 2, to which
-      // the others' are added. A warp always has the same tasks (every turn, or every
-      // second, fourth, ... where there are fewer tasks than warps), so what they
-      // need is worked out once for the expert.
-      const int groups_log2 = kN == 1 || (kFmt == MOE_W_MXFP4 && rows <= 8) ? 0 : 1;
-      const int tasks_log2 = 4 - s.split_log2 + groups_log2 + wide, tasks = 1 << tasks_log2;
-      const int turns_mask = tasks < kWarps ? (kWarps >> tasks_log2) - 1 : 0, my_turn = (warp >> tasks_log2) & turns_mask;
-      constexpr int kTasks = kN;  // at most, of a warp
-      struct Task {
-        bool mine, on;       // there is one, of a group with tokens; this lane's sum is of one of them
-        int m;               // granule of the turn
-        const float* part;   // first of the sums' parts, in the first buffer
-        float scale, gate;
-        const uint16_t* bias;
-        int64_t out;         // element of h or o, for granule 0
-      } task[kTasks];
-      uint16_t bias[kTasks];
+      // A turn's granules are finished by some of the warps, each always with the
+      // same task (every second, fourth, ... turn where there are fewer tasks than
+      // warps), so what it needs is worked out once for the expert. A task is a sum a
+      // lane: of a fragment's 128 elements 32, of those of the first of the 4 or 2
+      // units, to which the others' are added. For more than 8 MXFP4 tokens it is a
+      // whole fragment, four sums a lane, the units' added across the lanes, which
+      // then share out the columns (9 tokens 121 -> 105 us, but 7 tokens 88 -> 92).
+      constexpr bool kMx = kFmt == MOE_W_MXFP4, kWhole = kMx && kN == 2;
+      constexpr int kCols = kWhole ? 2 : 1;  // tokens of a lane
+      const int groups_log2 = kN == 1 || (kMx && rows <= 8) ? 0 : 1;
+      const int quarters_log2 = kWhole ? 0 : wide;
+      const int tasks_log2 = 4 - s.split_log2 + groups_log2 + quarters_log2;
+      const int turns_mask = (kWarps >> tasks_log2) - 1, my_turn = warp >> tasks_log2;
+      const int id = warp & ((1 << tasks_log2) - 1);
+      const int grp = (id >> quarters_log2) & ((1 << groups_log2) - 1), m = id >> (quarters_log2 + groups_log2);
+      const bool mine = 8 * grp < rows;
+      // the lane's first element of the fragment, and its weight row
+      const int el = (id & ((1 << quarters_log2) - 1)) * 32 + lane, frag = el / 4;
+      const int at = kWhole ? lane * 4 : ((frag >> wide) * 4 + (frag & ((1 << wide) - 1))) * 4 + el % 4;
+      const int r = at / 16 + (at & 2 ? 8 : 0);
+      const int pick = wide == 1 ? fq >> 1 : fq & 1;  // whole, up to 4 tokens: the lane's column of its two
+      const float* const part = red + ((m << s.split_log2) * kN + grp) * 128 + at;
+      const int bias_at = e * s.rows + (r < 8 ? r : s.up + r - 8);  // (at most 256 x 131072)
+      const uint16_t* const bias_base = which == 1 ? p.b1 : p.b2;
+      bool on[kCols];
+      float scale[kCols], gate[kCols];
+      int out[kCols];  // element of h or o, for granule 0 (at most 128 x 65536)
 #pragma unroll
-      for (int i = 0; i < kTasks; ++i) {
-        const int id = (warp & (tasks - 1)) + kWarps * i;
-        const int grp = (id >> wide) & ((1 << groups_log2) - 1);
-        // fragment element -> weight row r and token n
-        const int el = (id & ((1 << wide) - 1)) * 32 + lane, frag = el / 4;
-        const int at = ((frag >> wide) * 4 + (frag & ((1 << wide) - 1))) * 4 + el % 4;
-        const int r = at / 16 + (at & 2 ? 8 : 0), n = 8 * grp + (at / 4 % 4) * 2 + (at & 1);
-        task[i].mine = id < tasks && 8 * grp < rows;
-        task[i].m = id >> (wide + groups_log2);
-        task[i].on = task[i].mine && n < rows;
+      for (int c = 0; c < kCols; ++c) {
+        const int col = !kWhole     ? at / 4 % 4 * 2 + (at & 1)
+                        : wide == 2 ? 2 * fq + c
+                        : wide == 1 ? 2 * (fq & 1) + pick
+                                    : pick;
+        const int n = 8 * grp + col;
+        // (an up half's lane of its own writes nothing: its gate's lane writes h)
+        on[c] = mine && n < rows && (kWhole ? wide == 2 || (c == 0 && (wide == 1 || fq < 2)) : which == 2 || r < 8);
         const int row = start + (n < rows ? n : 0), a = sh.slot[row];
-        task[i].part = red + ((task[i].m << s.split_log2) * kN + grp) * 128 + at;
-        task[i].scale = kFmt == MOE_W_BF16 ? 1.0f : sh.row_scale[which == 1 ? sh.token[row] : row - start];
-        task[i].gate = sh.gate[a];
-        task[i].bias = which == 1 ? p.b1 + static_cast<int64_t>(e) * 2 * p.I + (r < 8 ? r : p.I + r - 8)
-                                  : p.b2 + static_cast<int64_t>(e) * p.D + r;
-        task[i].out = which == 1 ? static_cast<int64_t>(row) * p.I + r : static_cast<int64_t>(a) * p.D + r;
-        if (which == 1 && r >= 8) task[i].on = false;  // an up half: its gate's lane writes h
+        scale[c] = kMx ? sh.row_scale[which == 1 ? sh.token[row] : row - start] : 1.0f;
+        gate[c] = sh.gate[a];
+        out[c] = (which == 1 ? row * p.I : a * p.D) + r;
       }
+      uint16_t bias[2];
       // What the finish needs from memory, asked for a turn ahead.
       auto load_bias = [&](int first, int turn) {
-        if ((turn & turns_mask) != my_turn) return;
-#pragma unroll
-        for (int i = 0; i < kTasks; ++i) {
-          const int local = first + task[i].m;
-          if (task[i].mine && local < end) bias[i] = task[i].bias[local * s.step];
-        }
+        if ((turn & turns_mask) != my_turn || !mine || first + m >= end) return;
+        bias[0] = bias_base[bias_at + (first + m) * s.step];
+        if (kWhole) bias[1] = bias_base[bias_at + (first + m) * s.step + s.up];
       };
       auto finish = [&](int first, int turn) {
         const int buf = turn & (p.red_bufs - 1);
         const bool active = (turn & turns_mask) == my_turn;
-        float sum[kTasks];
+        float sum[kWhole ? 4 : 1];
         if (active) {
           wait_local(full_at + 8 * buf, (turn >> buf_shift) & 1, sh, p.header);
 #pragma unroll
-          for (int i = 0; i < kTasks; ++i) {
-            sum[i] = 0.0f;
-            if (task[i].mine) {
-              const float* part = task[i].part + buf * kRedFloats;
+          for (int c = 0; c < (kWhole ? 4 : 1); ++c) sum[c] = 0.0f;
+          if (mine) {
+            const float* from = part + buf * kRedFloats;
+            if constexpr (kWhole) {
+#pragma unroll 1
+              for (int w = 0; w < 1 << s.split_log2; w += 4) {
+                float4 v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const float4*>(from + (w + i) * (kN * 128));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  sum[0] += v[i].x;
+                  sum[1] += v[i].y;
+                  sum[2] += v[i].z;
+                  sum[3] += v[i].w;
+                }
+              }
+            } else {
               for (int c = 0; c < 16; c += 4 << wide) {
 #pragma unroll 4
-                for (int w = 0; w < 1 << s.split_log2; ++w) sum[i] += part[w * (kN * 128) + c];
+                for (int w = 0; w < 1 << s.split_log2; ++w) sum[0] += from[w * (kN * 128) + c];
               }
             }
           }
           __syncwarp();
         }
         if (lane == 0) sm100::mbar_arrive(empty_at + 8 * buf);
-        if (!active) return;
+        const int local = first + m;
+        if (!active || !mine || local >= end) return;  // (uniform in a warp)
+        if constexpr (kWhole) {
 #pragma unroll
-        for (int i = 0; i < kTasks; ++i) {
-          const int local = first + task[i].m;
-          if (!task[i].mine || local >= end) continue;  // (uniform in a warp)
-          const float v = fmaf(sum[i], task[i].scale, bf16_bits_to_float(bias[i]));
+          for (int off = 2; off > 0; off /= 2)
+            if (wide < off)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], off);
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) {
+            if (c > 0 && wide < 2) break;
+            const bool second = wide == 2 ? c > 0 : pick != 0;
+            const float lo = fmaf(second ? sum[1] : sum[0], scale[c], bf16_bits_to_float(bias[0]));
+            const float hi = fmaf(second ? sum[3] : sum[2], scale[c], bf16_bits_to_float(bias[1]));
+            if (!on[c]) continue;
+            if (which == 1) {
+              p.h[out[c] + local * 8] = float_to_bf16_bits(glu_act(lo, hi, p.act));
+            } else {
+              p.o[out[c] + local * 16] = gate[c] * lo;
+              p.o[out[c] + local * 16 + 8] = gate[c] * hi;
+            }
+          }
+        } else {
+          const float v = fmaf(sum[0], scale[0], bf16_bits_to_float(bias[0]));
           if (which == 1) {
             const float up = __shfl_xor_sync(0xffffffffu, v, 2);
-            if (task[i].on) p.h[task[i].out + local * 8] = float_to_bf16_bits(glu_act(v, up, p.act));
-          } else if (task[i].on) {
-            p.o[task[i].out + local * 16] = task[i].gate * v;
+            if (on[0]) p.h[out[0] + local * 8] = float_to_bf16_bits(glu_act(v, up, p.act));
+          } else if (on[0]) {
+            p.o[out[0] + local * 16] = gate[0] * v;
           }
         }
       };
@@ -994,7 +1035,8 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
             const int chunk = i - s.side / 2 * s.nchunks;
             if (chunk >= 0 && chunk < s.nchunks && s.side < count) {
               // this warp's units of the stage, an even number
-              const int first = chunk * s.chunk, n = min(s.chunk, s.units - first), per = (n + (2 << s.split_log2) - 1) >> (s.split_log2 + 1) << 1;
+              const int first = chunk * s.chunk, n = min(s.chunk, s.units - first);
+              const int per = (n + (2 << s.split_log2) - 1) >> (s.split_log2 + 1) << 1;
               const int u0 = min(n, s.part * per);
               int left = min(n, u0 + per) - u0;
               const uint8_t* slab = ring + slot * p.slab_bytes;

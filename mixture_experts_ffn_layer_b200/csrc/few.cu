@@ -187,17 +187,19 @@ __device__ __forceinline__ void warps_sync() { asm volatile("bar.sync 1, %0;" ::
 __device__ __forceinline__ void loaders_sync() { asm volatile("bar.sync 2, %0;" ::"n"(32 * kLoaders) : "memory"); }
 
 // All blocks of the grid meet (the launch is cooperative, so all are
-// resident). Waits at most kBarrierNs, then records the timeout and goes on:
-// every index computed later is in range whatever the data hold.
-__device__ __forceinline__ void grid_barrier(unsigned* header, int which) {
+// resident): each arrives, and waits for the others at most kBarrierNs, then
+// records the timeout and goes on -- every index computed later is in range
+// whatever the data hold.
+__device__ __forceinline__ void grid_arrive(unsigned* header, int which) {
   warps_sync();
+  if (threadIdx.x == 0) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(header + which) : "memory");
+}
+__device__ __forceinline__ void grid_wait(unsigned* header, int which) {
   if (threadIdx.x == 0) {
-    unsigned* count = header + which;
-    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(count) : "memory");
     unsigned seen;
     uint64_t t0 = 0;
     for (uint32_t i = 1;; ++i) {
-      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(count) : "memory");
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(header + which) : "memory");
       if (seen >= gridDim.x) break;
       if ((i & 63u) == 0) {
         const uint64_t now = sm100::globaltimer_ns();
@@ -210,6 +212,10 @@ __device__ __forceinline__ void grid_barrier(unsigned* header, int which) {
     }
   }
   warps_sync();
+}
+__device__ __forceinline__ void grid_barrier(unsigned* header, int which) {
+  grid_arrive(header, which);
+  grid_wait(header, which);
 }
 
 // The last block to leave sets the counters back to zero for the next call
@@ -753,8 +759,9 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
       p.logits[at] = sum + bf16_bits_to_float(p.br[at % p.E]);
     }
   }
-  load_rows<kFmt, true>(p, sh, p.x, p.T, p.D, act);
-  grid_barrier(p.header, kBar1);
+  grid_arrive(p.header, kBar1);
+  load_rows<kFmt, true>(p, sh, p.x, p.T, p.D, act);  // while the others arrive
+  grid_wait(p.header, kBar1);
 
   // ---- top-k of every token (warp t), then the active experts
   if (warp < p.T) {

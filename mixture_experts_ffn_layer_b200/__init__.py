@@ -20,7 +20,7 @@ from ._binding import (  # noqa: F401
     Fp8Dims, fp8_dims, fp8_workspace_bytes, alloc_fp8_workspace, moe_fp8_matmul,
 )
 from .ep import CudaLocalOps, ExpertParallelMoE, ep_forward  # noqa: F401,E402
-from .block import MoEBlock, fp8_matmul, rmsnorm, rmsnorm_fp8  # noqa: F401,E402
+from .block import _on, MoEBlock, fp8_matmul, rmsnorm, rmsnorm_fp8  # noqa: F401,E402
 
 
 class MoELayer:
@@ -81,10 +81,15 @@ class MoELayer:
         are read as stored, so the layer keeps their codes and scales."""
         if x.dim() != 2 or x.shape[1] != self.D or x.dtype != torch.bfloat16 or not x.is_contiguous():
             raise ValueError("x must be a contiguous (T, D) bf16 tensor")
+        if x.device != self.Wr.device:
+            raise ValueError("x must be on the layer's device")
+        if out is not None and (out.shape != x.shape or out.dtype != x.dtype or not out.is_contiguous() or
+                                out.device != x.device):
+            raise ValueError("out must be a contiguous tensor of x's shape and type, on its device")
         T = x.shape[0]
         y = out if out is not None else torch.empty_like(x)
-        moe_forward_few(self.dims(T), x, self.Wr, self.br, self.W1, self.b1, self.W2, self.b2, y, self.workspace(T),
-                        W1_scales=self.W1_scales, W2_scales=self.W2_scales, stream=stream)
+        _on(x.device, moe_forward_few, self.dims(T), x, self.Wr, self.br, self.W1, self.b1, self.W2, self.b2, y,
+            self.workspace(T), self.W1_scales, self.W2_scales, stream)
         return y
 
     def device_status(self) -> int:

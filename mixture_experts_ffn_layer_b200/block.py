@@ -124,6 +124,6 @@ class MoEBlock:
         if T == 0:
             return n, s
         few = T <= self.layer.few_max_tokens
-        return (self.layer.forward_few if few else self.layer.forward)(n, stream=stream), s
+        return _on(x.device, lambda: (self.layer.forward_few if few else self.layer.forward)(n, stream=stream)), s
 
     __call__ = forward

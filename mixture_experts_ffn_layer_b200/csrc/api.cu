@@ -3,6 +3,7 @@
 // grouped_gemm_pair.cu, mx_gemm.cu, norm.cu, few.cu and fp8_gemm.cu on the
 // caller's stream.
 // No host synchronisation except in moe_read_device_status.
+#include <algorithm>
 #include <cmath>
 
 #include "common.cuh"
@@ -47,7 +48,9 @@ WsLayout ws_layout(const moe_dims_t& d) {
     L.h_sf = take(mx_sf_bytes(d, d.I));
     L.mx_prep = take(mx_prep_bytes(d));
   }
-  if (d.T <= few_max_tokens(d)) L.few_logits = take(static_cast<size_t>(d.T) * d.E * 4);  // the one-launch layer
+  // the one-launch layer; beyond its tokens too, so that a workspace for more
+  // tokens is enough for fewer
+  L.few_logits = take(static_cast<size_t>(std::min(d.T, few_max_tokens(d))) * d.E * 4);
   L.total = off;
   return L;
 }

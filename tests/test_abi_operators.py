@@ -84,6 +84,27 @@ def test_forward_few_arguments():
     assert call(**q, w1=W(w1, None, s1), w2=W(w2, s2)) == 1
 
 
+def test_workspace_for_more_tokens_is_enough_for_fewer():
+    # around the one-launch layer's limit, where its logits could weigh more
+    # than another token's rows
+    for wfmt in (moe.MOE_W_BF16, moe.MOE_W_MXFP4):
+        n = [moe.workspace_bytes(moe.dims(T, 64, 256, 1, 64, wfmt=wfmt)) for T in range(1, 40)]
+        assert n == sorted(n), wfmt
+
+
+def test_forward_few_tensor_checks():
+    E, D, I = 4, 64, 64
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    layer = moe.MoELayer(z(E, D), z(E), z(E, 2 * I, D), z(E, 2 * I), z(E, D, I), z(E, D), 2)
+    x = z(3, D)
+    for bad in (z(3, D + 8), z(3, 2 * D)[:, ::2], x.float(), z(D), x.to("meta")):
+        with pytest.raises(ValueError):
+            layer.forward_few(bad)
+    for bad in (z(2, D), z(3, 2 * D)[:, :D], x.float(), x.to("meta")):
+        with pytest.raises(ValueError):
+            layer.forward_few(x, out=bad)
+
+
 def test_fp8_sizes_and_arguments():
     lib = moe.load()
     D = moe.fp8_dims

@@ -26,9 +26,10 @@
 // tile would leave the SMs unevenly loaded -- and the tensor rate is far from
 // being a limit. The k index of an MMA is permuted (lane q of a row's four holds
 // 8 consecutive elements of a 32-element unit), the same for weights and
-// activations, so both are read with wide shared-memory loads. The warps' partial
-// sums meet in shared memory behind mbarriers (full / empty per buffer): some of
-// the warps add them in warp order and finish the granule a turn later.
+// activations, so that the activations are read with wide shared-memory loads. The
+// warps' partial sums meet in shared memory behind mbarriers (full / empty per
+// buffer): some of the warps add them in warp order and finish the granule a turn
+// later.
 //
 // bf16: each warp streams its own slices through its own cp.async ring, with no
 // synchronisation between the warps to load.
@@ -41,7 +42,11 @@
 // become f16 (exact), the activations f16 with one power of two per row such that
 // the largest magnitude is in [2^8, 2^9) (exact down to 2^-25 of it, absolute
 // error below 2^-33 of it), and each unit's fp32 sum is added with its weight
-// scale.
+// scale. An expert with one or two tokens, the usual case of a decode step, would
+// leave most columns of an MMA empty: the columns then hold the activations of 4
+// units (of 2 for three or four tokens), loaded once for all of them, and each
+// unit's MMA is right in its own columns (that and ldmatrix for the codes: 8
+// tokens, D = 4096, I = 1536, 64 experts 68 -> 58 us).
 //
 // All sums are fp32. The order is fixed by the sizes, so results are bitwise
 // reproducible.
@@ -49,15 +54,17 @@
 // Measured, D = I = 2880, top-4 (the weights' bytes at the measured copy rate in
 // brackets; a kernel that only reads needs 36 us for one token's 199 MB of bf16
 // weights and about 15 for its 53 MB of MXFP4): 32 experts, bf16, 1 token 48 us
-// (30), 16 tokens 250 (224); MXFP4, 1 token 28 us (8); 128 experts, MXFP4, 7
-// tokens 98 us (54). What is left: about 7 us in front of the weights (router,
-// barrier, lists), 2.5 us at each later barrier, and for MXFP4 the codes'
-// conversion and multiplication, which take as long as the memory does and overlap
-// it only in part. Measured and not kept: 24 warps for MXFP4 (72 registers: no
-// faster), two granules per warp sharing the activations' loads (mlp1 41 -> 49
-// us), row-by-row copies of the codes (60 ns each: 49 -> 60), a router worked out
-// by every block in place of the first barrier (4.1 -> 10.9 us: every SM reads the
-// same weights from cold).
+// (30), 16 tokens 242 (220); MXFP4, 1 token 28 us (8); 128 experts, MXFP4, 7
+// tokens 86 us (52). What is left: about 7 us in front of one token's weights (10
+// for 7 tokens and 128 experts: router, barrier, lists), 2.5 us at each later
+// barrier; MXFP4 turns take 2.6 us where the memory needs 2.2 (without the
+// multiplications: 74 us). Measured and not kept: 24 warps for MXFP4 (72 registers:
+// no faster), a granule a stage (94 -> 108 us: twice the hand-overs), codes without
+// bank conflicts by exchanging units in registers (94 -> 102: the shared memory is
+// not what bounds), two granules per warp sharing the activations' loads (mlp1 41
+// -> 49 us), row-by-row copies of codes that lie well (60 ns each: 49 -> 60), a
+// router worked out by every block in place of the first barrier (4.1 -> 10.9 us:
+// every SM reads the same weights from cold).
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -918,11 +925,11 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
       const int r = at / 16 + (at & 2 ? 8 : 0);
       const int pick = wide == 1 ? fq >> 1 : fq & 1;  // whole, up to 4 tokens: the lane's column of its two
       const float* const part = red + ((m << s.split_log2) * kN + grp) * 128 + at;
-      const int bias_at = e * s.rows + (r < 8 ? r : s.up + r - 8);  // (at most 256 x 131072)
+      const int bias_at = e * s.rows + (r < 8 ? r : s.up + r - 8);  // (at most 256 x 32768)
       const uint16_t* const bias_base = which == 1 ? p.b1 : p.b2;
       bool on[kCols];
       float scale[kCols], gate[kCols];
-      int out[kCols];  // element of h or o, for granule 0 (at most 128 x 65536)
+      int out[kCols];  // element of h or o, for granule 0 (rows of 16384 at most)
 #pragma unroll
       for (int c = 0; c < kCols; ++c) {
         const int col = !kWhole     ? at / 4 % 4 * 2 + (at & 1)

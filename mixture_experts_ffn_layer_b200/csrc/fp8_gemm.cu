@@ -12,7 +12,8 @@
 // long; each alone would need 90 to 110 us for 8192 x 5760 x 2880, together,
 // handed over block by block through two TMEM buffers, they take 144 us (1.9
 // PFLOP/s in a burst; 168 us under the power cap). Few rows are bound by the
-// weights: 256 rows on 28 of 32 experts of 2880 x 2880 take 48 us (4.9 TB/s).
+// weights: 256 rows on 28 of 32 experts of 2880 x 2880 take 47 us (4.9 TB/s; 56
+// with cold caches).
 //
 // Measured and not kept: halves of a tile handed over separately (157 us against
 // 145), CTA pairs (291 us: both hand-overs of every block then cross CTAs),

@@ -106,6 +106,33 @@ def test_all_tokens_on_the_same_experts(wfmt):
     _close(y, _ref(inp))
 
 
+@pytest.mark.parametrize("wfmt", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("D,I", [(64, 64), (192, 320), (2880, 704), (1024, 2880)])
+def test_every_number_of_rows_per_expert(D, I, wfmt):
+    # every token on every expert: 1 to 16 rows each, over reductions of 2 to 90
+    # units of 32 that do not divide evenly among the warps
+    full = _make(16, D, 3, 3, I, wfmt)
+    ref = _ref(full)
+    for T in (1, 2, 3, 4, 5, 8, 9, 15, 16):
+        inp = dataclasses.replace(full, shape=dataclasses.replace(full.shape, T=T), x=full.x[:T].contiguous())
+        y, ws = _few(inp)
+        assert moe.moe_read_device_status(ws) == 0
+        _close(y, ref[:T])
+
+
+@pytest.mark.parametrize("T", [2, 4, 7])
+def test_nonfinite_token_among_those_of_its_experts(T):
+    # the tokens share an MMA's columns with several units of the reduction
+    inp = _make(T, 320, 2, 2, 192, "mxfp4")
+    ref = _ref(inp)
+    inp.x[1, 5] = float("nan")
+    inp.x[1, 300] = float("inf")
+    y, _ = _few(inp)
+    keep = [t for t in range(T) if t != 1]
+    _close(y[keep], ref[keep])
+    assert bool(torch.isnan(y[1]).all())
+
+
 def test_ties_go_to_the_lower_expert():
     inp = _make(6, 128, 40, 3, 64, "bf16")
     inp.Wr.zero_()

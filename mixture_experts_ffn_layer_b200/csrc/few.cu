@@ -37,8 +37,8 @@
 // MXFP4: the granules are a quarter of the size and the work on a byte four
 // times as much, so instructions and hand-overs count: other warps bring pairs
 // of granules in by bulk copies (the 16 spend nothing on loads), and the warps
-// work on two or four granules at a time, 16 / that many on each, which leaves
-// fewer partial sums to add. A unit of 32 codes is one scale block. The codes
+// work on four granules at a time (a turn), four on each, which leaves fewer
+// partial sums to add (two granules a turn: 81 -> 92 us for 7 tokens). A unit of 32 codes is one scale block. The codes
 // become f16 (exact), the activations f16 with one power of two per row such that
 // the largest magnitude is in [2^8, 2^9) (exact down to 2^-25 of it, absolute
 // error below 2^-33 of it), and each unit's fp32 sum is added with its weight
@@ -308,6 +308,13 @@ __host__ __device__ constexpr int mx_stage_bytes(int units, int nchunks) {
   return (32 * (mx_pitch(units, nchunks, mx_chunk(units, nchunks)) + units) + 127) / 128 * 128;
 }
 
+// log2 of the warps that split a granule's reduction, and the granules that the
+// block works on at a time (a turn).
+template <int kFmt>
+constexpr int kSplitLog2 = kFmt == MOE_W_BF16 ? 4 : 2;
+template <int kFmt>
+constexpr int kTurn = kWarps >> kSplitLog2<kFmt>;
+
 // One weight's granules as this block and warp see them.
 struct Stream {
   int64_t row_bytes;     // of the weight
@@ -316,9 +323,7 @@ struct Stream {
   int up;                // row of the 9th weight row relative to the 1st (I: the up half; 8)
   int step;              // weight rows a granule advances by (8 or 16)
   int per_expert;        // granules per expert
-  int turn;              // granules that the block works on at a time, kWarps / turn warps on each
-  int split_log2;        // log2 of those warps
-  int side, part;        // this warp's granule of them, its part of the granule's reduction
+  int side, part;        // this warp's granule of a turn, its part of the granule's reduction
   int u0, u1;            // this warp's units of 32 of the reduction
   int units;             // units of the reduction
   int nchunks;           // stages per granule
@@ -340,12 +345,10 @@ __device__ __forceinline__ Stream make_stream(const FewParams& p, int which, int
   const uint32_t n = n_active * s.per_expert;  // at most 128 * 2048
   s.g0 = static_cast<int>(n * blockIdx.x / gridDim.x);
   s.g1 = static_cast<int>(n * (blockIdx.x + 1) / gridDim.x);
-  s.split_log2 = kFmt == MOE_W_BF16 ? 4 : n >= 4 * gridDim.x ? 2 : 3;
-  s.turn = kWarps >> s.split_log2;
-  s.side = warp >> s.split_log2;
-  s.part = warp & ((1 << s.split_log2) - 1);
+  s.side = warp >> kSplitLog2<kFmt>;
+  s.part = warp & ((1 << kSplitLog2<kFmt>) - 1);
   // bf16: this warp's units, two a stage
-  const int per = (s.units + (1 << s.split_log2) - 1) >> s.split_log2;
+  const int per = (s.units + (1 << kSplitLog2<kFmt>) - 1) >> kSplitLog2<kFmt>;
   s.u0 = min(s.units, s.part * per);
   s.u1 = min(s.units, s.u0 + per);
   s.nchunks = kFmt == MOE_W_BF16 ? (per + kBfUnits - 1) / kBfUnits : which == 1 ? p.nchunks1 : p.nchunks2;
@@ -429,10 +432,10 @@ __device__ __forceinline__ void mx_produce(const FewParams& p, FewShared& sh, co
     const Stream& st = which == 1 ? st1 : st2;
     const int pitch = mx_pitch(st.units, st.nchunks, st.chunk);
     const bool as_stored = mx_as_stored(st.units, st.nchunks), idle = as_stored && loader != 0;
-    int ai = st.g0 / st.per_expert, local = st.g0 % st.per_expert, in_turn = 0;
+    int ai = st.g0 / st.per_expert, local = st.g0 % st.per_expert;
     for (int g = st.g0; g < st.g1 && !failed;) {
       const int left = min(st.per_expert - local, st.g1 - g);  // of this expert
-      const int count = min(2, min(left, st.turn - in_turn));
+      const int count = min(2, left);
       // runs of neighbouring rows: W1's gate and up rows, W2's rows
       const int runs = which == 1 ? 2 : 1, run = count * (which == 1 ? 8 : 16);
       const int64_t row0 = static_cast<int64_t>(sh.expert[ai]) * st.rows + static_cast<int64_t>(local) * st.step;
@@ -467,13 +470,9 @@ __device__ __forceinline__ void mx_produce(const FewParams& p, FewShared& sh, co
       }
       g += count;
       local += count;
-      in_turn += count;
       if (local == st.per_expert) {
         local = 0;
         ++ai;
-        in_turn = 0;
-      } else if (in_turn == st.turn) {
-        in_turn = 0;
       }
     }
   }
@@ -669,6 +668,7 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
   uint8_t* act = smem;
   float* red = reinterpret_cast<float*>(smem + p.T * p.row_pitch);
   constexpr int kRedFloats = kWarps * 128 * kN;
+  constexpr int kSplit = kSplitLog2<kFmt>;
   uint8_t* ring = reinterpret_cast<uint8_t*>(red + p.red_bufs * kRedFloats);
   __shared__ FewShared sh;
 
@@ -914,7 +914,7 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
       constexpr int kCols = kWhole ? 2 : 1;  // tokens of a lane
       const int groups_log2 = kN == 1 || (kMx && rows <= 8) ? 0 : 1;
       const int quarters_log2 = kWhole ? 0 : wide;
-      const int tasks_log2 = 4 - s.split_log2 + groups_log2 + quarters_log2;
+      const int tasks_log2 = 4 - kSplit + groups_log2 + quarters_log2;
       const int turns_mask = (kWarps >> tasks_log2) - 1, my_turn = warp >> tasks_log2;
       const int id = warp & ((1 << tasks_log2) - 1);
       const int grp = (id >> quarters_log2) & ((1 << groups_log2) - 1), m = id >> (quarters_log2 + groups_log2);
@@ -924,7 +924,7 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
       const int at = kWhole ? lane * 4 : ((frag >> wide) * 4 + (frag & ((1 << wide) - 1))) * 4 + el % 4;
       const int r = at / 16 + (at & 2 ? 8 : 0);
       const int pick = wide == 1 ? fq >> 1 : fq & 1;  // whole, up to 4 tokens: the lane's column of its two
-      const float* const part = red + ((m << s.split_log2) * kN + grp) * 128 + at;
+      const float* const part = red + ((m << kSplit) * kN + grp) * 128 + at;
       const int bias_at = e * s.rows + (r < 8 ? r : s.up + r - 8);  // (at most 256 x 32768)
       const uint16_t* const bias_base = which == 1 ? p.b1 : p.b2;
       bool on[kCols];
@@ -963,7 +963,7 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
             const float* from = part + buf * kRedFloats;
             if constexpr (kWhole) {
 #pragma unroll 1
-              for (int w = 0; w < 1 << s.split_log2; w += 4) {
+              for (int w = 0; w < 1 << kSplit; w += 4) {
                 float4 v[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const float4*>(from + (w + i) * (kN * 128));
@@ -978,7 +978,7 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
             } else {
               for (int c = 0; c < 16; c += 4 << wide) {
 #pragma unroll 4
-                for (int w = 0; w < 1 << s.split_log2; ++w) sum[0] += from[w * (kN * 128) + c];
+                for (int w = 0; w < 1 << kSplit; ++w) sum[0] += from[w * (kN * 128) + c];
               }
             }
           }
@@ -1017,7 +1017,7 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
           }
         }
       };
-      for (int base = begin; base < end; base += s.turn, ++it) {
+      for (int base = begin; base < end; base += kTurn<kFmt>, ++it) {
         float acc[kN][4];
 #pragma unroll
         for (int i = 0; i < kN; ++i)
@@ -1043,14 +1043,14 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
           // Every warp waits for every stage of the turn, in order, and frees
           // it -- at once where its granule is not in it -- so that no slot's
           // phase passes a warp by.
-          const int count = min(s.turn, end - base);
+          const int count = min(kTurn<kFmt>, end - base);
           for (int i = 0; i < (count + 1) / 2 * s.nchunks; ++i) {
             wait_local(sm100::smem_u32(&sh.w_full[slot]), slab_phase, sh, p.header);
             const int chunk = i - s.side / 2 * s.nchunks;
             if (chunk >= 0 && chunk < s.nchunks && s.side < count) {
               // this warp's units of the stage, an even number
               const int first = chunk * s.chunk, n = min(s.chunk, s.units - first);
-              const int per = (n + (2 << s.split_log2) - 1) >> (s.split_log2 + 1) << 1;
+              const int per = (n + (2 << kSplit) - 1) >> (kSplit + 1) << 1;
               const int u0 = min(n, s.part * per);
               int left = min(n, u0 + per) - u0;
               const uint8_t* slab = ring + slot * p.slab_bytes;
@@ -1100,11 +1100,11 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
           load_bias(base, it);
           finish(base, it);
         } else {
-          if (base > begin) finish(base - s.turn, it - 1);
+          if (base > begin) finish(base - kTurn<kFmt>, it - 1);
           load_bias(base, it);
         }
       }
-      if (p.red_bufs > 1) finish(begin + (end - begin - 1) / s.turn * s.turn, it - 1);
+      if (p.red_bufs > 1) finish(begin + (end - begin - 1) / kTurn<kFmt> * kTurn<kFmt>, it - 1);
     }
   }
   cp_wait<0>();

@@ -876,7 +876,7 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
   const int buf_shift = p.red_bufs >> 1;  // log2 of 1, 2 or 4
   const uint32_t full_at = sm100::smem_u32(sh.full), empty_at = sm100::smem_u32(sh.empty);
   const int fr = lane / 4, fq = lane % 4;
-#pragma unroll 1
+#pragma unroll
   for (int which = 1; which <= 2; ++which) {
     const Stream& s = which == 1 ? st1 : st2;
     if (which == 2) grid_barrier(p.header, kBar2);  // h is complete

@@ -88,7 +88,7 @@ class MoELayer:
             raise ValueError("out must be a contiguous tensor of x's shape and type, on its device")
         T = x.shape[0]
         y = out if out is not None else torch.empty_like(x)
-        _on(x.device, moe_forward_few, self.dims(T), x, self.Wr, self.br, self.W1, self.b1, self.W2, self.b2, y,
+        _on(x, moe_forward_few, self.dims(T), x, self.Wr, self.br, self.W1, self.b1, self.W2, self.b2, y,
             self.workspace(T), self.W1_scales, self.W2_scales, stream)
         return y
 

@@ -18,35 +18,34 @@ def _require(cond: bool, what: str):
         raise ValueError(what)
 
 
-def _on(device: torch.device, call, *args):
-    """call(*args) with `device` current."""
-    if device.type == "cuda" and device.index == torch.cuda.current_device():
+def _on(t: torch.Tensor, call, *args):
+    """call(*args) with t's device current."""
+    if t.is_cuda and t.get_device() == torch.cuda.current_device():
         return call(*args)
-    with torch.cuda.device(device):
+    with torch.cuda.device(t.device):
         return call(*args)
 
 
 def _norm_dims(x: torch.Tensor, gamma: torch.Tensor, eps: float, residual: Optional[torch.Tensor]) -> B.NormDims:
     _require(x.dim() == 2 and x.dtype == BF16 and x.stride(1) == 1, "x must be a (T, D) bf16 tensor of dense rows")
     T, D = x.shape
-    _require(gamma.dtype == BF16 and gamma.dim() == 1 and gamma.shape[0] == D and gamma.is_contiguous() and
-             gamma.device == x.device, "gamma must be a (D,) bf16 tensor on x's device")
+    at = x.device
+    _require(gamma.dtype == BF16 and gamma.shape == (D,) and gamma.is_contiguous() and gamma.device == at,
+             "gamma must be a (D,) bf16 tensor on x's device")
     f32 = False
     if residual is not None:
         f32 = residual.dtype == torch.float32
-        _require((f32 or residual.dtype == BF16) and residual.shape == x.shape and residual.is_contiguous() and
-                 residual.device == x.device, "residual must be a contiguous (T, D) bf16 or fp32 tensor on x's device")
+        _require((f32 or residual.dtype == BF16) and residual.shape == (T, D) and residual.is_contiguous() and
+                 residual.device == at, "residual must be a contiguous (T, D) bf16 or fp32 tensor on x's device")
     return B.NormDims(T, D, x.stride(0) if T > 1 else max(D, 1), eps, B.MOE_T_F32 if f32 else B.MOE_T_BF16)
 
 
-def _like(out: Optional[torch.Tensor], of: Optional[torch.Tensor], dtype, what: str) -> Optional[torch.Tensor]:
-    """`out` checked against `of`'s shape and device, or a new tensor; None without `of`."""
-    if of is None:
-        _require(out is None, f"{what} without a residual")
-        return None
+def _like(out: Optional[torch.Tensor], of: Optional[torch.Tensor], what: str) -> Optional[torch.Tensor]:
+    """`out` checked against `of`'s shape, type and device, or a new tensor; None without `of`."""
     if out is None:
-        return torch.empty_like(of)
-    _require(out.shape == of.shape and out.dtype == dtype and out.is_contiguous() and out.device == of.device,
+        return None if of is None else torch.empty_like(of)
+    _require(of is not None, f"{what} without a residual")
+    _require(out.shape == of.shape and out.dtype == of.dtype and out.is_contiguous() and out.device == of.device,
              f"{what} must be a contiguous (T, D) tensor of its input's type, on its device")
     return out
 
@@ -58,9 +57,9 @@ def rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-5, residual: O
     y = RMSNorm(s) * gamma in bf16. Rows of x may be strided. ``res_out`` may
     be the residual itself."""
     n = _norm_dims(x, gamma, eps, residual)
-    y = _like(out, x, BF16, "out")
-    res = _like(res_out, residual, None if residual is None else residual.dtype, "res_out")
-    _on(x.device, B.moe_rmsnorm, n, x, residual, gamma, res, y, None, None, stream)
+    y = _like(out, x, "out")
+    res = _like(res_out, residual, "res_out")
+    _on(x, B.moe_rmsnorm, n, x, residual, gamma, res, y, None, None, stream)
     return y, res
 
 
@@ -73,8 +72,8 @@ def rmsnorm_fp8(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-5, residua
     T, D = x.shape
     q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
     scale = x.new_empty((T, -(-D // 128)), dtype=torch.float32)
-    res = _like(res_out, residual, None if residual is None else residual.dtype, "res_out")
-    _on(x.device, B.moe_rmsnorm, n, x, residual, gamma, res, None, q, scale, stream)
+    res = _like(res_out, residual, "res_out")
+    _on(x, B.moe_rmsnorm, n, x, residual, gamma, res, None, q, scale, stream)
     return q, scale, res
 
 
@@ -103,7 +102,7 @@ def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale:
     device = a.device
     for t in (a, a_scale, w, w_scale, ws, offsets, bias, out):
         _require(t is None or (t.is_contiguous() and t.device == device), "tensors must be contiguous and on one device")
-    _on(device, B.moe_fp8_matmul, B.fp8_dims(R, E, N, K, out.dtype), a, a_scale, offsets, w, w_scale, bias, out, ws,
+    _on(a, B.moe_fp8_matmul, B.fp8_dims(R, E, N, K, out.dtype), a, a_scale, offsets, w, w_scale, bias, out, ws,
         stream)
     return out
 
@@ -124,6 +123,6 @@ class MoEBlock:
         if T == 0:
             return n, s
         few = T <= self.layer.few_max_tokens
-        return _on(x.device, lambda: (self.layer.forward_few if few else self.layer.forward)(n, stream=stream)), s
+        return _on(x, lambda: (self.layer.forward_few if few else self.layer.forward)(n, stream=stream)), s
 
     __call__ = forward

@@ -54,11 +54,12 @@
 // Measured, D = I = 2880, top-4 (the weights' bytes at the measured copy rate in
 // brackets; a kernel that only reads needs 36 us for one token's 199 MB of bf16
 // weights and about 15 for its 53 MB of MXFP4): 32 experts, bf16, 1 token 48 us
-// (30), 16 tokens 242 (220); MXFP4, 1 token 28 us (8); 128 experts, MXFP4, 7
-// tokens 86 us (52). What is left: about 7 us in front of one token's weights (10
-// for 7 tokens and 128 experts: router, barrier, lists), 2.5 us at each later
-// barrier; MXFP4 turns take 2.6 us where the memory needs 2.2 (without the
-// multiplications: 74 us). Measured and not kept: 24 warps for MXFP4 (72 registers:
+// (30), 16 tokens 242 (220); MXFP4, 1 token 27 us (8); 128 experts, MXFP4, 7
+// tokens 78 us (52). What is left: about 6 us in front of one token's weights (9
+// for 7 tokens and 128 experts: router, barrier, lists), 2 us at each later
+// barrier and 2 to 3 of SMs that end unequally; MXFP4 turns take 2.3 us where the
+// memory needs 2.2. The loop over the two weights is unrolled: 81 -> 78 us,
+// though mlp2's first turn then fetches its code (1.5 us). Measured and not kept: 24 warps for MXFP4 (72 registers:
 // no faster), a granule a stage (94 -> 108 us: twice the hand-overs), codes without
 // bank conflicts by exchanging units in registers (94 -> 102: the shared memory is
 // not what bounds), two granules per warp sharing the activations' loads (mlp1 41

@@ -7,17 +7,21 @@
 // the block of the reduction, so a block's products are summed by the tensor
 // cores (tcgen05 kind::f8f6f4, fp32 in TMEM) and added to the running sum with
 // its scale by ordinary fp32 FMAs, out of TMEM into registers: one FMA per
-// output element and block. 256 columns of that take eight warps about 305
-// cycles, the tensor core 512 and its operands' way into shared memory about as
-// long; each alone would need 90 to 110 us for 8192 x 5760 x 2880, together,
-// handed over block by block through two TMEM buffers, they take 144 us (1.9
-// PFLOP/s in a burst; 168 us under the power cap). Few rows are bound by the
-// weights: 256 rows on 28 of 32 experts of 2880 x 2880 take 47 us (4.9 TB/s; 56
-// with cold caches).
+// output element and block. At 8192 x 5760 x 2880 the tensor core alone needs 98
+// to 107 us, reading the sums out of TMEM 98 (108 with their FMAs), the operands'
+// way out of L2 96; tensor core and sums, which share TMEM, 131, all together,
+// handed over block by block through two TMEM buffers, 140 (1.9 PFLOP/s in a
+// burst; 168 us under the power cap). A buffer's round -- products, commit, wait,
+// read, release, wait -- bounds it: the hand-overs of a block alone take some 1000
+// cycles, the read 400, the products 512. Few rows are bound by the weights: 256
+// rows on 28 of 32 experts of 2880 x 2880 take 47 us (4.9 TB/s; 56 with cold
+// caches).
 //
 // Measured and not kept: halves of a tile handed over separately (157 us against
 // 145), CTA pairs (291 us: both hand-overs of every block then cross CTAs),
-// sixteen warps of 64 columns for the sums (181 us against 160).
+// sixteen warps of 64 columns for the sums (181 us against 160), reads of 32
+// columns whose FMAs overlap the next (160 against 140: every read waits some 200
+// cycles).
 //
 // One persistent block per SM over tiles of 128 rows x kBN columns:
 //   warps 0, 3  TMA producers of the tile's 128 x 128 block of a (a box of 32
@@ -122,14 +126,16 @@ __device__ __forceinline__ void fma2(float& c0, float& c1, float s, uint32_t v0,
       : "f"(s), "r"(v0), "r"(v1));
 }
 
-// 32 lanes x 64 consecutive 32-bit columns per thread.
+// 32 lanes x 64 consecutive 32-bit columns per thread, waited for (in one
+// statement, so that no use of them can come before the wait).
 __device__ __forceinline__ void tmem_ld_x64(uint32_t taddr, uint32_t (&v)[64]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
       "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
       "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
       "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
-      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
         "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]),
         "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]),
@@ -144,6 +150,7 @@ __device__ __forceinline__ void tmem_ld_x64(uint32_t taddr, uint32_t (&v)[64]) {
       : "r"(taddr)
       : "memory");
 }
+
 // A tile's columns and the warps that hold its sums, and what follows.
 template <int kBN_, int kSumWarps_>
 struct Shape {
@@ -277,7 +284,8 @@ __global__ void __launch_bounds__(S_::kThreads, 1)
               break;
             }
             mbar_arrive_expect_tx(full_bar(stage), bytes);
-            tma_load_2d(smem_u32(smem + stage * kStageBytes) + (warp == 3 ? kABytes : 0), map, full_bar(stage), kb * BK, at);
+            tma_load_2d(smem_u32(smem + stage * kStageBytes) + (warp == 3 ? kABytes : 0), map, full_bar(stage),
+                        kb * BK, at);
             ++issued;
             if (++stage == S) {
               stage = 0;
@@ -310,8 +318,8 @@ __global__ void __launch_bounds__(S_::kThreads, 1)
         const uint32_t idesc = idesc_e4m3_f32(BM, min(kBN, p.N - nt * kBN));
         for (int kb = 0; kb < p.KB; ++kb, ++count) {
           if (static_cast<int>(count & 1u) == mine) {
-            if (!__all_sync(0xffffffffu, wait_bounded(tempty_bar(buf), buf_phase ^ 1u, abort_flag) &&
-                                             wait_bounded(full_bar(stage), phase, abort_flag))) {
+            if (!__all_sync(0xffffffffu, wait_bounded(full_bar(stage), phase, abort_flag) &&
+                                             wait_bounded(tempty_bar(buf), buf_phase ^ 1u, abort_flag))) {
               failed = true;
               break;
             }
@@ -323,8 +331,8 @@ __global__ void __launch_bounds__(S_::kThreads, 1)
             for (int kk = 0; kk < BK / 32; ++kk)
               mma_f8_elect(d_tmem, desc_kmajor_sw128(a_addr + kk * 32), desc_kmajor_sw128(b_addr + kk * 32), idesc,
                            kk != 0 ? 1u : 0u);
-            tc_commit_elect(empty_bar(stage));
             tc_commit_elect(tfull_bar(buf));
+            tc_commit_elect(empty_bar(stage));
           }
           if (++stage == S) {
             stage = 0;
@@ -432,7 +440,6 @@ __global__ void __launch_bounds__(S_::kThreads, 1)
 #pragma unroll
         for (int c = 0; c < kCols; c += 64) {
           tmem_ld_x64(from + buf * kBN + c, v);
-          tmem_ld_wait();
           if (c + 64 == kCols) {
             tc_fence_before();
             __syncwarp();

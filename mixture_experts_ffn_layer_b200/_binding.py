@@ -114,7 +114,7 @@ def _p(t: Optional[torch.Tensor]):
 
 def _stream(stream=None):
     if stream is None:  # (the raw handle: building a torch.cuda.Stream around it takes longer than a small launch)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
 
 

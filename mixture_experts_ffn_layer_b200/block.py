@@ -20,7 +20,7 @@ def _require(cond: bool, what: str):
 
 def _on(t: torch.Tensor, call, *args):
     """call(*args) with t's device current."""
-    if t.is_cuda and t.get_device() == torch.cuda.current_device():
+    if t.is_cuda and t.get_device() == torch._C._cuda_getDevice():  # (a device tensor: CUDA is initialised)
         return call(*args)
     with torch.cuda.device(t.device):
         return call(*args)
@@ -29,14 +29,14 @@ def _on(t: torch.Tensor, call, *args):
 def _norm_dims(x: torch.Tensor, gamma: torch.Tensor, eps: float, residual: Optional[torch.Tensor]) -> B.NormDims:
     _require(x.dim() == 2 and x.dtype == BF16 and x.stride(1) == 1, "x must be a (T, D) bf16 tensor of dense rows")
     T, D = x.shape
-    at = x.device
-    _require(gamma.dtype == BF16 and gamma.shape == (D,) and gamma.is_contiguous() and gamma.device == at,
+    at = x.get_device()
+    _require(gamma.dtype == BF16 and gamma.shape == (D,) and gamma.is_contiguous() and gamma.get_device() == at,
              "gamma must be a (D,) bf16 tensor on x's device")
     f32 = False
     if residual is not None:
         f32 = residual.dtype == torch.float32
         _require((f32 or residual.dtype == BF16) and residual.shape == (T, D) and residual.is_contiguous() and
-                 residual.device == at, "residual must be a contiguous (T, D) bf16 or fp32 tensor on x's device")
+                 residual.get_device() == at, "residual must be a contiguous (T, D) bf16 or fp32 tensor on x's device")
     return B.NormDims(T, D, x.stride(0) if T > 1 else max(D, 1), eps, B.MOE_T_F32 if f32 else B.MOE_T_BF16)
 
 
@@ -71,7 +71,7 @@ def rmsnorm_fp8(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-5, residua
     n = _norm_dims(x, gamma, eps, residual)
     T, D = x.shape
     q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
-    scale = x.new_empty((T, -(-D // 128)), dtype=torch.float32)
+    scale = x.new_empty(T, -(-D // 128), dtype=torch.float32)
     res = _like(res_out, residual, "res_out")
     _on(x, B.moe_rmsnorm, n, x, residual, gamma, res, None, q, scale, stream)
     return q, scale, res
@@ -85,9 +85,10 @@ def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale:
     fp32, as rmsnorm_fp8 gives the left operand. With ``offsets`` (E+1) int32
     the rows of [offsets[e], offsets[e+1]) are multiplied with w[e]; without,
     E = 1 and all rows are. ``bias`` (E, N) bf16. Returns (R, N)."""
-    _require(a.dim() == 2 and w.dim() == 3 and a.shape[1] == w.shape[2], "a must be (R, K) and w (E, N, K)")
-    R, K = a.shape
-    E, N, _ = w.shape
+    of_a, of_w = a.shape, w.shape
+    _require(len(of_a) == 2 and len(of_w) == 3 and of_a[1] == of_w[2], "a must be (R, K) and w (E, N, K)")
+    R, K = of_a
+    E, N, _ = of_w
     kb, nb = -(-K // 128), -(-N // 128)
     _require(a.dtype == torch.float8_e4m3fn and w.dtype == torch.float8_e4m3fn, "a and w must be float8_e4m3fn")
     _require(a_scale.dtype == torch.float32 and w_scale.dtype == torch.float32 and a_scale.shape == (R, kb) and
@@ -97,11 +98,13 @@ def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale:
     _require(bias is None or (bias.shape == (E, N) and bias.dtype == BF16), "bias must be (E, N) bf16")
     if out is None:
         _require(out_dtype in (BF16, torch.float32), "out_dtype must be bf16 or fp32")
-        out = a.new_empty((R, N), dtype=out_dtype)
-    _require(out.shape == (R, N) and out.dtype in (BF16, torch.float32), "out must be (R, N) bf16 or fp32")
-    device = a.device
+        out = a.new_empty(R, N, dtype=out_dtype)
+    else:
+        _require(out.shape == (R, N) and out.dtype in (BF16, torch.float32), "out must be (R, N) bf16 or fp32")
+    at = a.get_device()
     for t in (a, a_scale, w, w_scale, ws, offsets, bias, out):
-        _require(t is None or (t.is_contiguous() and t.device == device), "tensors must be contiguous and on one device")
+        if t is not None and (t.get_device() != at or not t.is_contiguous()):
+            raise ValueError("tensors must be contiguous and on one device")
     _on(a, B.moe_fp8_matmul, B.fp8_dims(R, E, N, K, out.dtype), a, a_scale, offsets, w, w_scale, bias, out, ws,
         stream)
     return out

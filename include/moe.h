@@ -214,10 +214,12 @@ MOE_API moe_status_t moe_forward(moe_dims_t d, const uint16_t* x, const uint16_t
  * weights (a scale byte of 0, 2^-127, counts as zero; 255 is an infinity).
  * Equal logits go to the lower expert index, a NaN logit below every
  * number; an infinity or NaN in a token's row reaches only that token's
- * output. x and y must not overlap. Deterministic for given sizes; its sums are ordered differently from
- * moe_forward's. The kernel needs every SM of the device at once: it starts
- * when the kernels before it on the device have left enough room (another
- * stream's long kernel delays it). Returns MOE_ERR_UNSUPPORTED for more
+ * output. x and y must not overlap. Deterministic for given sizes; its sums
+ * are ordered differently from moe_forward's. The kernel needs every SM of
+ * the device at once: it starts when the kernels before it on the device have
+ * left enough room (another stream's long kernel delays it), and gives up,
+ * with MOE_ERR_TIMEOUT in the status word, where its blocks wait for one
+ * another for more than a second. Returns MOE_ERR_UNSUPPORTED for more
  * tokens. */
 MOE_API moe_status_t moe_forward_few(moe_dims_t d, const uint16_t* x, const uint16_t* Wr, const uint16_t* br,
                              moe_weight_t W1, const uint16_t* b1, moe_weight_t W2, const uint16_t* b2,
@@ -284,7 +286,8 @@ typedef struct {
  * Products are summed in fp32 within a block (tensor cores) and over the
  * blocks; one rounding to bf16 at the end. Deterministic for given sizes.
  * R >= 0 (R = 0: nothing is enqueued) up to 2^30, E <= 256, N and K multiples
- * of 16 up to 65536, fewer than 2^31 tiles (ceil(R/128) + E) * ceil(N/64). ws: at least moe_fp8_workspace_bytes(d) (the device status word; any
+ * of 16 up to 65536, fewer than 2^31 tiles (ceil(R/128) + E) * ceil(N/64).
+ * ws: at least moe_fp8_workspace_bytes(d) (the device status word; any
  * workspace of this library is large enough). Offsets that do not ascend
  * within [0, R] record MOE_ERR_DEVICE_BOUNDS and write nothing. */
 MOE_API moe_status_t moe_check_fp8(moe_fp8_t d);

@@ -299,3 +299,28 @@ def test_two_host_threads():
     assert bad == []
     for _, ws in want:
         assert moe.moe_read_device_status(ws) == 0
+
+
+def test_two_graphs_at_once():
+    # captured calls with a workspace each, replayed on two streams at once
+    cases = [_make(2, 512, 16, 4, 512, "mxfp4"), _make(9, 448, 8, 2, 704, "bf16")]
+    want = [_few(c) for c in cases]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for c, (y, ws) in zip(cases, want):
+        out, graph = torch.zeros_like(y), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(5):
+                _few(c, ws=ws, y=out)
+        graphs.append(graph)
+        outs.append(out)
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for out, (y, ws) in zip(outs, want):
+        assert moe.moe_read_device_status(ws) == 0
+        assert torch.equal(out, y)

@@ -20,14 +20,15 @@ from ._binding import (  # noqa: F401
     Fp8Dims, fp8_dims, fp8_workspace_bytes, alloc_fp8_workspace, moe_fp8_matmul,
 )
 from .ep import CudaLocalOps, ExpertParallelMoE, ep_forward  # noqa: F401,E402
-from .block import _on, MoEBlock, fp8_matmul, rmsnorm, rmsnorm_fp8  # noqa: F401,E402
+from .block import _on, _under, MoEBlock, fp8_matmul, rmsnorm, rmsnorm_fp8  # noqa: F401,E402
 
 
 class MoELayer:
     """One MoE FFN layer's weights on the device plus its workspace.
 
     ``forward(x)`` enqueues the whole layer (moe_forward) on the current
-    stream and returns y (T, D) bf16. Weights: Wr (E,D), br (E), W1 (E,2I,D),
+    stream, or on ``stream`` with buffers of that stream, and returns y (T, D)
+    bf16. Weights: Wr (E,D), br (E), W1 (E,2I,D),
     b1 (E,2I), W2 (E,D,I), b2 (E,D) bf16 -- or W1/W2 as MXFP4 codes with
     ``W1_scales``/``W2_scales``. ``act`` is MOE_ACT_SWIGLU or MOE_ACT_GPTOSS
     (with the caller's ``act_alpha`` and ``act_limit``)."""
@@ -61,10 +62,12 @@ class MoELayer:
         return self._ws
 
     def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        if stream is not None:
+            return _under(stream, x, self.forward, x, out)
         T = x.shape[0]
         y = out if out is not None else torch.empty((T, self.D), dtype=torch.bfloat16, device=x.device)
         moe_forward(self.dims(T), x, self.Wr, self.br, self.W1, self.b1, self.W2, self.b2, y, self.workspace(T),
-                    W1_scales=self.W1_scales, W2_scales=self.W2_scales, stream=stream, W1_prepared=self.W1_prepared,
+                    W1_scales=self.W1_scales, W2_scales=self.W2_scales, W1_prepared=self.W1_prepared,
                     W2_prepared=self.W2_prepared)
         return y
 
@@ -79,6 +82,8 @@ class MoELayer:
         """forward for at most few_max_tokens tokens in one launch
         (moe_forward_few): the latency path of a decode step. MXFP4 weights
         are read as stored, so the layer keeps their codes and scales."""
+        if stream is not None:
+            return _under(stream, x, self.forward_few, x, out)
         if x.dim() != 2 or x.shape[1] != self.D or x.dtype != torch.bfloat16 or not x.is_contiguous():
             raise ValueError("x must be a contiguous (T, D) bf16 tensor")
         if x.device != self.Wr.device:
@@ -89,7 +94,7 @@ class MoELayer:
         T = x.shape[0]
         y = out if out is not None else torch.empty_like(x)
         _on(x, moe_forward_few, self.dims(T), x, self.Wr, self.br, self.W1, self.b1, self.W2, self.b2, y,
-            self.workspace(T), self.W1_scales, self.W2_scales, stream)
+            self.workspace(T), self.W1_scales, self.W2_scales)
         return y
 
     def device_status(self) -> int:

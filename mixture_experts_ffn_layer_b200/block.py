@@ -1,7 +1,11 @@
 """What stands around the MoE layer in a transformer block: the residual's
 addition and RMSNorm in front of it (write-up, "model flow"), with outputs in
 bf16 or block-scaled E4M3, and ``MoEBlock``, which runs the norm and the layer
-together."""
+together.
+
+A call with ``stream`` runs on that stream and takes its buffers from it; the
+inputs must be ready there (``stream.wait_stream``) and stay until it is done, as
+for any use of a tensor on a second stream."""
 from __future__ import annotations
 
 from typing import Optional, Tuple
@@ -24,6 +28,21 @@ def _on(t: torch.Tensor, call, *args):
         return call(*args)
     with torch.cuda.device(t.device):
         return call(*args)
+
+
+def _under(stream, at: torch.Tensor, call, *args, **kw):
+    """call(*args, **kw) with `stream` current, so that what the call allocates
+    is that stream's; what it returns is marked as used on the caller's too."""
+    _require(stream.device == at.device, "stream must be one of the tensors' device")
+    caller = torch.cuda.current_stream(stream.device)
+    if caller == stream:
+        return call(*args, **kw)
+    with torch.cuda.stream(stream):
+        got = call(*args, **kw)
+    for t in got if isinstance(got, tuple) else (got,):
+        if t is not None:
+            t.record_stream(caller)
+    return got
 
 
 def _norm_dims(x: torch.Tensor, gamma: torch.Tensor, eps: float, residual: Optional[torch.Tensor]) -> B.NormDims:
@@ -56,10 +75,12 @@ def rmsnorm(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-5, residual: O
     """(y, s): s = x + residual in the residual's type (None without one) and
     y = RMSNorm(s) * gamma in bf16. Rows of x may be strided. ``res_out`` may
     be the residual itself."""
+    if stream is not None:
+        return _under(stream, x, rmsnorm, x, gamma, eps, residual, out, res_out)
     n = _norm_dims(x, gamma, eps, residual)
     y = _like(out, x, "out")
     res = _like(res_out, residual, "res_out")
-    _on(x, B.moe_rmsnorm, n, x, residual, gamma, res, y, None, None, stream)
+    _on(x, B.moe_rmsnorm, n, x, residual, gamma, res, y, None, None)
     return y, res
 
 
@@ -68,12 +89,14 @@ def rmsnorm_fp8(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-5, residua
                 stream=None) -> Tuple[torch.Tensor, torch.Tensor, Optional[torch.Tensor]]:
     """(q, q_scale, s): as rmsnorm with y quantised to E4M3, one fp32 scale
     per row and 128 columns."""
+    if stream is not None:
+        return _under(stream, x, rmsnorm_fp8, x, gamma, eps, residual, res_out)
     n = _norm_dims(x, gamma, eps, residual)
     T, D = x.shape
     q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
     scale = x.new_empty(T, -(-D // 128), dtype=torch.float32)
     res = _like(res_out, residual, "res_out")
-    _on(x, B.moe_rmsnorm, n, x, residual, gamma, res, None, q, scale, stream)
+    _on(x, B.moe_rmsnorm, n, x, residual, gamma, res, None, q, scale)
     return q, scale, res
 
 
@@ -85,6 +108,8 @@ def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale:
     fp32, as rmsnorm_fp8 gives the left operand. With ``offsets`` (E+1) int32
     the rows of [offsets[e], offsets[e+1]) are multiplied with w[e]; without,
     E = 1 and all rows are. ``bias`` (E, N) bf16. Returns (R, N)."""
+    if stream is not None:
+        return _under(stream, a, fp8_matmul, a, a_scale, w, w_scale, ws, offsets, bias, out, out_dtype)
     of_a, of_w = a.shape, w.shape
     _require(len(of_a) == 2 and len(of_w) == 3 and of_a[1] == of_w[2], "a must be (R, K) and w (E, N, K)")
     R, K = of_a
@@ -105,8 +130,7 @@ def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale:
     for t in (a, a_scale, w, w_scale, ws, offsets, bias, out):
         if t is not None and (t.get_device() != at or not t.is_contiguous()):
             raise ValueError("tensors must be contiguous and on one device")
-    _on(a, B.moe_fp8_matmul, B.fp8_dims(R, E, N, K, out.dtype), a, a_scale, offsets, w, w_scale, bias, out, ws,
-        stream)
+    _on(a, B.moe_fp8_matmul, B.fp8_dims(R, E, N, K, out.dtype), a, a_scale, offsets, w, w_scale, bias, out, ws)
     return out
 
 
@@ -121,11 +145,13 @@ class MoEBlock:
         self.layer, self.gamma, self.eps = layer, gamma, eps
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
-        n, s = rmsnorm(x, self.gamma, self.eps, residual=residual, stream=stream)
+        if stream is not None:  # (the normed rows between the two are the stream's own)
+            return _under(stream, x, self.forward, x, residual)
+        n, s = rmsnorm(x, self.gamma, self.eps, residual=residual)
         T = x.shape[0]
         if T == 0:
             return n, s
         few = T <= self.layer.few_max_tokens
-        return _on(x, lambda: (self.layer.forward_few if few else self.layer.forward)(n, stream=stream)), s
+        return _on(x, lambda: (self.layer.forward_few if few else self.layer.forward)(n)), s
 
     __call__ = forward

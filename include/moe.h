@@ -215,7 +215,11 @@ MOE_API moe_status_t moe_forward(moe_dims_t d, const uint16_t* x, const uint16_t
  * Equal logits go to the lower expert index, a NaN logit below every
  * number; an infinity or NaN in a token's row reaches only that token's
  * output. x and y must not overlap. Deterministic for given sizes; its sums
- * are ordered differently from moe_forward's. The kernel needs every SM of
+ * are ordered differently from moe_forward's. ws: the bytes for the same sizes
+ * with wfmt = MOE_W_BF16 are enough. It holds the counters with which the
+ * blocks wait for one another: its zero-fill has to be done, not only recorded
+ * into a graph, before the first call, and a graph that holds the call needs it
+ * to stay where it is. The kernel needs every SM of
  * the device at once: it starts when the kernels before it on the device have
  * left enough room (another stream's long kernel delays it), and gives up,
  * with MOE_ERR_TIMEOUT in the status word, where its blocks wait for one

@@ -44,6 +44,14 @@ class MoELayer:
         self.act, self.act_alpha, self.act_limit = act, act_alpha, act_limit
         self._ws: Optional[torch.Tensor] = None
         self._ws_T = 0
+        # forward_few's workspace holds the counters of its grid barriers. It is made
+        # and zeroed here and never replaced: a first call on another stream or
+        # inside a capture finds it zeroed, and a captured call finds it in place
+        # after forward has taken a larger one. (A bf16 layer's is enough.)
+        self._few_ws: Optional[torch.Tensor] = None
+        most = self.few_max_tokens
+        if most:
+            self._few_ws = alloc_workspace(dims(most, self.D, self.E, k, self.I), device=Wr.device)
         # MXFP4 weights: their prepare-once form (scale layout of the
         # block-scaled MMAs), made here so that no call repeats it
         self.W1_prepared = self.W2_prepared = None
@@ -51,6 +59,8 @@ class MoELayer:
             d1 = self.dims(1)
             self.W1_prepared = mxfp4_prepare(d1, 1, W1, W1_scales)
             self.W2_prepared = mxfp4_prepare(d1, 2, W2, W2_scales)
+        if Wr.is_cuda and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(Wr.device).synchronize()
 
     def dims(self, T: int) -> Dims:
         return dims(T, self.D, self.E, self.k, self.I, self.wfmt, self.act, self.act_alpha, self.act_limit)
@@ -93,9 +103,13 @@ class MoELayer:
             raise ValueError("out must be a contiguous tensor of x's shape and type, on its device")
         T = x.shape[0]
         y = out if out is not None else torch.empty_like(x)
+        ws = self._few_ws if self._few_ws is not None else self.workspace(T)  # (which refuses what has none)
         _on(x, moe_forward_few, self.dims(T), x, self.Wr, self.br, self.W1, self.b1, self.W2, self.b2, y,
-            self.workspace(T), self.W1_scales, self.W2_scales)
+            ws, self.W1_scales, self.W2_scales)
         return y
 
     def device_status(self) -> int:
-        return 0 if self._ws is None else moe_read_device_status(self._ws)
+        """Read and clear the status words of the layer's workspaces: the first
+        error recorded since the last call, 0 if none."""
+        status = [moe_read_device_status(ws) for ws in (self._few_ws, self._ws) if ws is not None]
+        return next((st for st in status if st), 0)

@@ -15,7 +15,7 @@ namespace {
 
 struct WsLayout {
   size_t block_counts, topk_idx, topk_w, counts, offsets, perm, inv, x_perm, h, o_perm, xq, x_sf, hq, h_sf,
-      mx_prep, route_partial, few_logits, total;
+      mx_prep, route_partial, few_logits, few_total, total;
 };
 
 WsLayout ws_layout(const moe_dims_t& d) {
@@ -39,6 +39,10 @@ WsLayout ws_layout(const moe_dims_t& d) {
   L.o_perm = take(static_cast<size_t>(R) * d.D * 4);
   if (route_splits(d) > 1)  // K-split router: fp32 partial logits per split
     L.route_partial = take(static_cast<size_t>(route_splits(d)) * d.T * ((d.E + 15) / 16 * 16) * 4);
+  // the one-launch layer; beyond its tokens too, so that a workspace for more
+  // tokens is enough for fewer
+  L.few_logits = take(static_cast<size_t>(std::min(d.T, few_max_tokens(d))) * d.E * 4);
+  L.few_total = off;
   if (d.wfmt == MOE_W_MXFP4) {
     // block-scaled MMA operands: the routed rows and h as hi/lo E4M3 pairs
     // plus their tile-blocked E8M0 scales (the expert weights are used as stored)
@@ -48,9 +52,6 @@ WsLayout ws_layout(const moe_dims_t& d) {
     L.h_sf = take(mx_sf_bytes(d, d.I));
     L.mx_prep = take(mx_prep_bytes(d));
   }
-  // the one-launch layer; beyond its tokens too, so that a workspace for more
-  // tokens is enough for fewer
-  L.few_logits = take(static_cast<size_t>(std::min(d.T, few_max_tokens(d))) * d.E * 4);
   L.total = off;
   return L;
 }
@@ -279,8 +280,9 @@ moe_status_t moe_forward_few(moe_dims_t d, const uint16_t* x, const uint16_t* Wr
   MOE_TRY(check_weight(d, W1));
   MOE_TRY(check_weight(d, W2));
   MOE_REQUIRE(d.wfmt == MOE_W_BF16 || (W1.scales && W2.scales));  // the weights are read as stored
-  MOE_TRY(check_ws(d, ws, ws_bytes));
+  MOE_REQUIRE(ws && aligned32(ws));
   const WsLayout L = ws_layout(d);
+  if (ws_bytes < L.few_total) return MOE_ERR_WORKSPACE;
   return launch_few(d, x, Wr, br, W1, b1, W2, b2, y, at<float>(ws, L.few_logits), at<uint16_t>(ws, L.h),
                     at<float>(ws, L.o_perm), ws, static_cast<cudaStream_t>(stream));
 }

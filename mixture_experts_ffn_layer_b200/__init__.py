@@ -23,6 +23,15 @@ from .ep import CudaLocalOps, ExpertParallelMoE, ep_forward  # noqa: F401,E402
 from .block import _on, _under, MoEBlock, fp8_matmul, rmsnorm, rmsnorm_fp8  # noqa: F401,E402
 
 
+def _capturing(t: torch.Tensor) -> bool:
+    return t.is_cuda and torch.cuda.is_current_stream_capturing()
+
+
+def _stream_id(t: torch.Tensor) -> int:
+    """The current stream of t's device."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else 0
+
+
 class MoELayer:
     """One MoE FFN layer's weights on the device plus its workspace.
 
@@ -43,7 +52,11 @@ class MoELayer:
         self.wfmt = MOE_W_BF16 if W1_scales is None else MOE_W_MXFP4
         self.act, self.act_alpha, self.act_limit = act, act_alpha, act_limit
         self._ws: Optional[torch.Tensor] = None
-        self._ws_T = 0
+        self._ws_T: Optional[int] = None  # tokens of the last call
+        self._ws_home = 0          # the stream it was allocated on
+        self._ws_captured = False  # a graph holds it
+        self._ws_recorded = False  # its zero-fill was recorded into a graph, not run
+        self._kept = []            # workspaces that graphs hold
         # forward_few's workspace holds the counters of its grid barriers. It is made
         # and zeroed here and never replaced: a first call on another stream or
         # inside a capture finds it zeroed, and a captured call finds it in place
@@ -66,9 +79,22 @@ class MoELayer:
         return dims(T, self.D, self.E, self.k, self.I, self.wfmt, self.act, self.act_alpha, self.act_limit)
 
     def workspace(self, T: int) -> torch.Tensor:
-        if self._ws is None or self._ws_T < T:
+        """forward's workspace for T tokens, to be used on the current stream."""
+        capturing = _capturing(self.Wr)
+        if T != self._ws_T and (self._ws is None or self._ws.numel() < workspace_bytes(self.dims(T))):
+            if self._ws_captured:
+                self._kept.append(self._ws)
             self._ws = alloc_workspace(self.dims(T), device=self.Wr.device)
-            self._ws_T = T
+            self._ws_home, self._ws_captured, self._ws_recorded = _stream_id(self.Wr), False, capturing
+        self._ws_T = T
+        if capturing:
+            self._ws_captured = True
+            return self._ws
+        if self._ws_recorded:
+            self._ws[:256].zero_()  # the status word's part
+            self._ws_recorded = False
+        if self._ws_home != _stream_id(self.Wr):
+            self._ws.record_stream(torch.cuda.current_stream(self.Wr.device))
         return self._ws
 
     def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -76,9 +102,8 @@ class MoELayer:
             return _under(stream, x, self.forward, x, out)
         T = x.shape[0]
         y = out if out is not None else torch.empty((T, self.D), dtype=torch.bfloat16, device=x.device)
-        moe_forward(self.dims(T), x, self.Wr, self.br, self.W1, self.b1, self.W2, self.b2, y, self.workspace(T),
-                    W1_scales=self.W1_scales, W2_scales=self.W2_scales, W1_prepared=self.W1_prepared,
-                    W2_prepared=self.W2_prepared)
+        moe_forward(self.dims(T), x, self.Wr, self.br, self.W1, self.b1, self.W2, self.b2, y,
+                    self.workspace(T), self.W1_scales, self.W2_scales, None, self.W1_prepared, self.W2_prepared)
         return y
 
     __call__ = forward
@@ -111,5 +136,5 @@ class MoELayer:
     def device_status(self) -> int:
         """Read and clear the status words of the layer's workspaces: the first
         error recorded since the last call, 0 if none."""
-        status = [moe_read_device_status(ws) for ws in (self._few_ws, self._ws) if ws is not None]
+        status = [moe_read_device_status(ws) for ws in (self._few_ws, self._ws, *self._kept) if ws is not None]
         return next((st for st in status if st), 0)

@@ -1,6 +1,8 @@
 """The workspaces that MoELayer keeps: what a call on another stream, a captured
 one, or one for more tokens leaves to the others."""
 import ctypes
+import gc
+import weakref
 
 import pytest
 import torch
@@ -63,6 +65,95 @@ def test_layer_without_a_one_launch_form():
     assert layer._few_ws is None
     with pytest.raises(moe.MoeError):
         layer.forward_few(torch.zeros((2, 96), dtype=BF16))
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_larger_batch_keeps_a_captured_workspace(captured, used, monkeypatch):
+    # what a graph writes to when it is replayed is not given back; what none
+    # holds is
+    layer, capturing = _layer(), [captured]
+    monkeypatch.setattr(moe, "_capturing", lambda t: capturing[0])
+    layer.forward(torch.zeros((40, 64), dtype=BF16))
+    capturing[0] = False
+    before = weakref.ref(used[0])
+    used.clear()
+    layer.forward(torch.zeros((500, 64), dtype=BF16))
+    gc.collect()
+    assert (before() is not None) == captured
+    assert before() is None or before() is not used[0]
+
+
+def test_workspace_recorded_into_a_graph_is_zeroed_for_other_calls(used, monkeypatch):
+    # its zero-fill was recorded, not run
+    layer, capturing = _layer(), [True]
+    monkeypatch.setattr(moe, "_capturing", lambda t: capturing[0])
+    x = torch.zeros((40, 64), dtype=BF16)
+    layer.forward(x)
+    used[0].fill_(7)
+    capturing[0] = False
+    layer.forward(x)
+    assert used[1] is used[0] and not bool(used[1][:256].any())
+    used[1][0] = 5  # an error that a kernel recorded
+    layer.forward(x)
+    assert int(used[2][0]) == 5
+
+
+def test_workspace_is_marked_used_on_other_streams(used, monkeypatch):
+    layer, at, marked = _layer(), [11], []
+    monkeypatch.setattr(moe, "_stream_id", lambda t: at[0])
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: at[0])
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda self, s: marked.append(s), raising=False)
+    x = torch.zeros((40, 64), dtype=BF16)
+    layer.forward(x)
+    assert marked == []
+    at[0] = 12
+    layer.forward(x)
+    assert marked == [12]
+
+
+def test_workspace_for_more_tokens_that_is_smaller(used):
+    # beyond 18 tiles of 128 tokens the router keeps no partial sums
+    more, fewer = 18 * 128 + 1, 18 * 128
+    need = [moe.workspace_bytes(moe.dims(T, 512, 64, 1, 64)) for T in (more, fewer)]
+    assert need[0] < need[1]
+    layer = _layer(E=64, D=512, k=1)
+    for T in (more, fewer):
+        layer.forward(torch.zeros((T, 512), dtype=BF16))
+    assert [ws.numel() for ws in used] == need
+
+
+@pytest.mark.gpu
+def test_captured_batch_outlives_a_larger_one():
+    layer = _layer(E=8, D=320, I=192, device="cuda")
+    x, big = (torch.randn((T, 320), device="cuda").to(BF16) for T in (40, 4000))
+    want, y = layer(x), torch.zeros_like(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer.forward(x, out=y)
+    n = layer._ws.numel()
+    big_y = layer(big)
+    others = [torch.full((n,), i + 1, dtype=torch.uint8, device="cuda") for i in range(8)]
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.equal(layer(big), big_y)
+    for i, t in enumerate(others):
+        assert bool((t == i + 1).all())
+    assert layer.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_first_batch_in_a_graph():
+    layer = _layer(E=8, D=320, I=192, device="cuda")
+    x = torch.randn((40, 320), device="cuda").to(BF16)
+    want, y = _layer(E=8, D=320, I=192, device="cuda")(x), torch.zeros_like(x)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer.forward(x, out=y)
+    assert torch.equal(layer(x), want) and layer.device_status() == 0
+    graph.replay()
+    assert torch.equal(y, want) and layer.device_status() == 0
 
 
 @pytest.mark.gpu

@@ -102,8 +102,8 @@ class MoELayer:
             return _under(stream, x, self.forward, x, out)
         T = x.shape[0]
         y = out if out is not None else torch.empty((T, self.D), dtype=torch.bfloat16, device=x.device)
-        moe_forward(self.dims(T), x, self.Wr, self.br, self.W1, self.b1, self.W2, self.b2, y,
-                    self.workspace(T), self.W1_scales, self.W2_scales, None, self.W1_prepared, self.W2_prepared)
+        _on(x, moe_forward, self.dims(T), x, self.Wr, self.br, self.W1, self.b1, self.W2, self.b2, y,
+            self.workspace(T), self.W1_scales, self.W2_scales, None, self.W1_prepared, self.W2_prepared)
         return y
 
     __call__ = forward
@@ -133,8 +133,11 @@ class MoELayer:
             ws, self.W1_scales, self.W2_scales)
         return y
 
-    def device_status(self) -> int:
-        """Read and clear the status words of the layer's workspaces: the first
-        error recorded since the last call, 0 if none."""
-        status = [moe_read_device_status(ws) for ws in (self._few_ws, self._ws, *self._kept) if ws is not None]
+    def device_status(self, stream=None) -> int:
+        """Wait for the current stream, or ``stream``, then read and clear the
+        status words of the layer's workspaces: an error recorded since the last
+        call, 0 if none. (After a first call inside a capture: not before the
+        graph has run.)"""
+        status = [_on(ws, moe_read_device_status, ws, stream) for ws in (self._few_ws, self._ws, *self._kept)
+                  if ws is not None]
         return next((st for st in status if st), 0)

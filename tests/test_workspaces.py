@@ -111,6 +111,17 @@ def test_workspace_is_marked_used_on_other_streams(used, monkeypatch):
     assert marked == [12]
 
 
+def test_calls_run_with_the_layers_device_current(monkeypatch):
+    where = []
+    monkeypatch.setattr(moe, "_on", lambda t, call, *args, **kw: where.append((t.device, call)) or 0)
+    layer, x = _layer(), torch.zeros((3, 64), dtype=BF16)
+    layer.forward(x)
+    layer.forward_few(x)
+    layer.device_status()
+    assert [call for _, call in where] == [moe.moe_forward, moe.moe_forward_few] + 2 * [moe.moe_read_device_status]
+    assert all(device == x.device for device, _ in where)
+
+
 def test_workspace_for_more_tokens_that_is_smaller(used):
     # beyond 18 tiles of 128 tokens the router keeps no partial sums
     more, fewer = 18 * 128 + 1, 18 * 128
@@ -154,6 +165,22 @@ def test_first_batch_in_a_graph():
     assert torch.equal(layer(x), want) and layer.device_status() == 0
     graph.replay()
     assert torch.equal(y, want) and layer.device_status() == 0
+
+
+@pytest.mark.gpu
+def test_status_of_another_stream():
+    layer = _layer(E=8, D=320, I=192, device="cuda")
+    x = torch.randn((40, 320), device="cuda").to(BF16)
+    want = layer(x)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(2_000_000)
+    y2 = layer(x, stream=side)
+    # an error on that stream, seen by reading the status there
+    moe.moe_selftest_wait_timeout(layer._ws, 1000, stream=side)
+    assert layer.device_status(side) == 5
+    assert torch.equal(y2, want) and layer.device_status() == 0
 
 
 @pytest.mark.gpu

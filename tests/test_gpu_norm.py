@@ -148,3 +148,30 @@ def test_other_stream_and_graph():
     graph.replay()
     want_y, want_s = moe.rmsnorm(x2, gamma, residual=residual)
     assert torch.equal(y, want_y) and torch.equal(s, want_s)
+
+
+def test_quotients_next_to_a_border():
+    # rows of +-1 leave y = +-gamma exactly, and c = 49 / 448 is a number of few
+    # bits: gamma = 7/64 * m has the quotient m exactly, half-way between two
+    # neighbours of E4M3 for these m, and goes to the even one. (y * (448 / 49) in
+    # fp32 lies above half-way for m = 23 and up.)
+    D = 256
+    m = torch.arange(17, 33, 2, device="cuda", dtype=F32)
+    gamma = torch.full((D,), 7 / 64, device="cuda")
+    for block in (0, 128):
+        gamma[block] = 49.0
+        gamma[block + 1:block + 9] = 7 / 64 * m
+        gamma[block + 9:block + 17] = 7 / 64 * m / 8
+    assert torch.equal(gamma.to(BF16).float(), gamma)
+    x = torch.ones((3, D), dtype=BF16, device="cuda")
+    x[1] = -1.0
+    x[2, ::2] = -1.0
+    q, scale, _ = moe.rmsnorm_fp8(x, gamma.to(BF16), 0.0)
+    assert bool((scale == 49 / 448).all())
+    even = torch.tensor([16, 20, 20, 24, 24, 28, 28, 32], device="cuda", dtype=F32)  # of 17, 19, ... 31
+    for row in range(3):
+        for block in (0, 128):
+            sign = x[row, block + 1:block + 9].float()
+            assert torch.equal(q[row, block + 1:block + 9].float(), sign * even)
+            sign = x[row, block + 9:block + 17].float()
+            assert torch.equal(q[row, block + 9:block + 17].float(), sign * even / 8)

@@ -258,7 +258,9 @@ typedef struct {
  *      q (T,D) E4M3 and q_scale (T, ceil(D/128)) fp32 (may both be NULL): per
  *      row and 128 columns c = max(max|y|, 2^-100) / 448, q = e4m3(y / c),
  *      rounded to nearest even from the fp32 y -- the left operand of
- *      moe_fp8_matmul. A NaN in a row makes that row NaN.
+ *      moe_fp8_matmul. A NaN in a row makes that row NaN, its scales too; an
+ *      infinity becomes NaN, and so do its block's scale and codes, beside which
+ *      the rest of the row is zero.
  * At least one of y and q is given. No buffer but residual / res_out may
  * overlap another. T >= 0 (T = 0: nothing is enqueued), D a multiple of 16 up
  * to 16384, ldx >= D a multiple of 16, eps >= 0 and finite. Needs no

@@ -56,6 +56,13 @@ __device__ __forceinline__ void pack16(const float (&f)[kVec], uint32_t (&w)[8])
   for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
 }
 
+// The larger of two; a NaN stays.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
 // y / c for two y from inv, about 1 / c: first quotients and one Newton step with
 // their remainders, which the FMA gives exactly. A quotient of few bits, such as
 // one half-way between two E4M3 values, comes out exactly; y * inv alone can lie
@@ -141,7 +148,7 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_kernel(const NormParams p
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
         v[j][i] = v[j][i] * rstd * f[i];
-        amax = fmaxf(amax, fabsf(v[j][i]));
+        amax = max_nan(amax, fabsf(v[j][i]));
       }
       if (p.y) {
         uint32_t w[8];
@@ -151,9 +158,9 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_kernel(const NormParams p
     }
     if (p.q) {  // (uniform: every lane takes part in the shuffles)
 #pragma unroll
-      for (int off = 4; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+      for (int off = 4; off > 0; off >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, off));
       if (on) {
-        amax = fmaxf(amax, kAmaxMin);
+        amax = max_nan(amax, kAmaxMin);
         const float c = amax / kE4m3Max, inv = kE4m3Max / amax;
         const float back = isinf(c) ? 0.0f : c;
         uint32_t w[4];

@@ -175,3 +175,32 @@ def test_quotients_next_to_a_border():
             assert torch.equal(q[row, block + 1:block + 9].float(), sign * even)
             sign = x[row, block + 9:block + 17].float()
             assert torch.equal(q[row, block + 9:block + 17].float(), sign * even / 8)
+
+
+def test_nonfinite_values_reach_the_scale():
+    # c = max|y| / 448 of a block with a NaN is NaN, and so are its codes
+    D = 384
+    x = torch.ones((4, D), dtype=BF16, device="cuda")
+    x[0, 200] = float("nan")
+    x[1, 130] = float("inf")
+    x[2, 383] = float("-inf")
+    gamma = torch.ones(D, dtype=BF16, device="cuda")
+    y, _ = moe.rmsnorm(x, gamma)
+    q, scale, _ = moe.rmsnorm_fp8(x, gamma)
+    assert bool(torch.isnan(y[0]).all()) and bool(torch.isnan(q[0].float()).all())
+    assert bool(torch.isnan(scale[0]).all())
+    for row, col in ((1, 130), (2, 383)):
+        bad = torch.arange(D, device="cuda") // 128 == col // 128
+        assert bool(torch.isnan(y[row, col])) and int(torch.isnan(y[row]).sum()) == 1
+        assert torch.equal(torch.isnan(scale[row]), bad[::128])
+        assert torch.equal(torch.isnan(q[row].float()), bad)
+        assert bool((q[row].float()[~bad] == 0).all())
+        assert bool((scale[row][~bad[::128]].double() - 2.0 ** -100 / 448).abs().max() <= 2.0 ** -120)
+    # y beyond fp32: an infinite scale, beside which finite y are zero
+    gamma[5] = 3e38
+    x[3, 5] = 8.0
+    q, scale, _ = moe.rmsnorm_fp8(x[3:], gamma)
+    assert bool(torch.isinf(scale[0, 0])) and bool(torch.isnan(q[0, 5].float()))
+    keep = [c for c in range(128) if c != 5]
+    assert bool((q[0].float()[keep] == 0).all())
+    assert bool(torch.isfinite(scale[0, 1:]).all()) and bool((q[0].float()[128:] == 448).all())

@@ -75,7 +75,7 @@ typedef enum { MOE_W_BF16 = 0, MOE_W_MXFP4 = 1 } moe_wfmt_t;
  *     on the grouped experts' SwiGLU variant): gc = min(g, act_limit),
  *     uc = min(max(u, -act_limit), act_limit), h = gc * sigmoid(act_alpha * gc) * (uc + 1).
  *     The pages do not give alpha and limit; the caller does (act_limit may be
- *     +inf for no clamping). Ignored for MOE_ACT_SWIGLU. */
+ *     +inf for no clamping); a NaN stays NaN. Ignored for MOE_ACT_SWIGLU. */
 typedef enum { MOE_ACT_SWIGLU = 0, MOE_ACT_GPTOSS = 1 } moe_act_t;
 
 typedef struct {

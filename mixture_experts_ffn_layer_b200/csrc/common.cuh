@@ -29,6 +29,18 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return static_cast<uint32_t>(float_to_bf16_bits(lo)) | (static_cast<uint32_t>(float_to_bf16_bits(hi)) << 16);
 }
 
+// The larger and the smaller of two; a NaN stays.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float m;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
 // Launch helpers shared by the host side of every .cu file.
 struct Launch {
   cudaStream_t stream;
@@ -57,8 +69,8 @@ struct Act {
 
 __device__ __forceinline__ float glu_act(float g, float u, const Act& a) {
   if (a.kind == MOE_ACT_SWIGLU) return __fdividef(g, 1.0f + __expf(-g)) * u;
-  const float gc = fminf(g, a.limit);
-  const float uc = fminf(fmaxf(u, -a.limit), a.limit);
+  const float gc = min_nan(g, a.limit);
+  const float uc = min_nan(max_nan(u, -a.limit), a.limit);
   return __fdividef(gc, 1.0f + __expf(-a.alpha * gc)) * (uc + 1.0f);
 }
 

@@ -56,13 +56,6 @@ __device__ __forceinline__ void pack16(const float (&f)[kVec], uint32_t (&w)[8])
   for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
 }
 
-// The larger of two; a NaN stays.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float m;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
-  return m;
-}
-
 // y / c for two y from inv, about 1 / c: first quotients and one Newton step with
 // their remainders, which the FMA gives exactly. A quotient of few bits, such as
 // one half-way between two E4M3 values, comes out exactly; y * inv alone can lie

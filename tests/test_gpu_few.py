@@ -324,3 +324,29 @@ def test_two_graphs_at_once():
     for out, (y, ws) in zip(outs, want):
         assert moe.moe_read_device_status(ws) == 0
         assert torch.equal(out, y)
+
+
+@pytest.mark.parametrize("T", [5, 12, 40, 300])
+@pytest.mark.parametrize("wfmt", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("half", ["gate", "up"])
+def test_nan_of_an_expert_passes_the_clamps(half, wfmt, T):
+    # a NaN in one expert's bias reaches every token of that expert and no other,
+    # through the GPT-OSS activation too, few tokens or many
+    inp = _make(T, 256, 8, 2, 128, wfmt)
+    _, idx, w = oracle.route(inp.x, inp.Wr, inp.br, 2)
+    expert = int(idx[0, 0])
+    inp.b1[expert, 7 if half == "gate" else 128 + 7] = float("nan")
+    hit = (idx == expert).any(1)
+    assert not bool(hit.all())
+    d = dims_of(inp, GPTOSS)
+    if T <= 16:
+        y, ws = _few(inp, GPTOSS)
+    else:
+        y, ws = torch.empty_like(inp.x), moe.alloc_workspace(d)
+        moe.moe_forward(d, inp.x, inp.Wr, inp.br, inp.W1, inp.b1, inp.W2, inp.b2, y, ws, W1_scales=inp.W1_scales,
+                        W2_scales=inp.W2_scales)
+    assert moe.moe_read_device_status(ws) == 0
+    assert torch.equal(torch.isnan(y).all(1).cpu(), hit) and not bool(torch.isnan(y.cpu()[~hit]).any())
+    if T <= 16:
+        ref = _ref(dataclasses.replace(inp, b1=torch.nan_to_num(inp.b1)), GPTOSS)
+        _close(y.cpu()[~hit], ref[~hit])

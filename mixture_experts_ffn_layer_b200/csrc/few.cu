@@ -628,12 +628,13 @@ __device__ __forceinline__ void load_rows(const FewParams& p, FewShared& sh, con
       float mul[kAtOnce];
 #pragma unroll
       for (int z = 0; z < kAtOnce; ++z) {
-        // 2^shift brings the row's largest magnitude into [2^8, 2^9); a row of
-        // zeros, or with an infinity or NaN, stays as it is
+        // 2^shift brings the row's largest magnitude into [2^8, 2^9); with an
+        // infinity or NaN the largest there can be beside it, so that finite
+        // values do not become infinite in f16; a row of zeros stays as it is
         const int n = min(n0 + z, rows - 1);
         const uint32_t largest = sh.row_max[n];
-        const int ex = static_cast<int>(largest >> 7);  // biased exponent
-        const int shift = largest == 0 || ex == 255 ? 0 : min(127, 8 + 127 - max(ex, 1));
+        const int ex = min(static_cast<int>(largest >> 7), 254);  // biased exponent
+        const int shift = largest == 0 ? 0 : min(127, 8 + 127 - max(ex, 1));
         mul[z] = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
         if (threadIdx.x == 0)
           sh.row_scale[n] = __uint_as_float(shift == 127 ? 0x00400000u : static_cast<uint32_t>(127 - shift) << 23);

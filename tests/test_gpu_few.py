@@ -350,3 +350,31 @@ def test_nan_of_an_expert_passes_the_clamps(half, wfmt, T):
     if T <= 16:
         ref = _ref(dataclasses.replace(inp, b1=torch.nan_to_num(inp.b1)), GPTOSS)
         _close(y.cpu()[~hit], ref[~hit])
+
+
+@pytest.mark.parametrize("wfmt", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("T", [1, 6, 16])
+def test_infinite_hidden_unit_beside_large_finite_ones(T, wfmt):
+    # h from the biases alone: one unit overflows to infinity, another is -1e30;
+    # outputs that weigh both with 1 or -1 are infinite, not NaN
+    D, I = 128, 64
+    inp = _make(T, D, 1, 1, I, wfmt)
+    inp.b1.zero_()
+    inp.b1[0, 0], inp.b1[0, I] = 1e30, 1e30
+    inp.b1[0, 1], inp.b1[0, I + 1] = 1e20, -1e10
+    inp.b2.zero_()
+    inp.W1.zero_()
+    if wfmt == "mxfp4":
+        inp.W1_scales.fill_(127)
+        inp.W2_scales.fill_(127)
+        inp.W2.zero_()
+        inp.W2[0, ::2, 0] = 0x22   # codes of 1 for units 0 and 1
+        inp.W2[0, 1::2, 0] = 0xAA  # of -1
+    else:
+        inp.W2.zero_()
+        inp.W2[0, ::2, :2], inp.W2[0, 1::2, :2] = 1.0, -1.0
+    y, ws = _few(inp)
+    assert moe.moe_read_device_status(ws) == 0
+    want = torch.full((T, D), float("inf"), dtype=BF16, device="cuda")
+    want[:, 1::2] *= -1
+    assert torch.equal(y, want)

@@ -138,20 +138,28 @@ class MoEBlock:
     """The feed-forward half of a transformer block: residual addition,
     RMSNorm and the MoE layer. ``forward(x, residual)`` returns (y, s) with
     s = x + residual, the residual stream, and y = layer(RMSNorm(s) * gamma),
-    which the next block adds to s. Batches of at most ``layer.few_max_tokens``
-    tokens take the one-launch layer."""
+    which the next block adds to s. The first block of a model has no residual
+    (None): s is x, in the same buffer where its rows are dense.
+
+    ``layer`` is a MoELayer, whose batches of at most ``layer.few_max_tokens``
+    tokens take the one-launch layer: MXFP4 weights then meet activations that
+    are more exact than the batched layer's pairs of E4M3, so a row's result can
+    depend on the batch's size by more than the sums' order."""
 
     def __init__(self, layer, gamma: torch.Tensor, eps: float = 1e-5):
         self.layer, self.gamma, self.eps = layer, gamma, eps
 
-    def forward(self, x: torch.Tensor, residual: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor],
+                stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
         if stream is not None:  # (the normed rows between the two are the stream's own)
             return _under(stream, x, self.forward, x, residual)
         n, s = rmsnorm(x, self.gamma, self.eps, residual=residual)
+        if residual is None:
+            s = x.contiguous()
         T = x.shape[0]
         if T == 0:
             return n, s
         few = T <= self.layer.few_max_tokens
-        return _on(x, lambda: (self.layer.forward_few if few else self.layer.forward)(n)), s
+        return _on(x, self.layer.forward_few if few else self.layer.forward, n), s
 
     __call__ = forward

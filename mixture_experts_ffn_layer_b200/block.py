@@ -141,10 +141,12 @@ class MoEBlock:
     which the next block adds to s. The first block of a model has no residual
     (None): s is x, in the same buffer where its rows are dense.
 
-    ``layer`` is a MoELayer, whose batches of at most ``layer.few_max_tokens``
-    tokens take the one-launch layer: MXFP4 weights then meet activations that
-    are more exact than the batched layer's pairs of E4M3, so a row's result can
-    depend on the batch's size by more than the sums' order."""
+    ``layer`` is a MoELayer or an ExpertParallelMoE; the latter is called with no
+    tokens too, since every rank takes part in it. A MoELayer's batches of at
+    most ``few_max_tokens`` tokens take the one-launch layer: MXFP4 weights then
+    meet activations that are more exact than the batched layer's pairs of E4M3,
+    so a row's result can depend on the batch's size by more than the sums'
+    order."""
 
     def __init__(self, layer, gamma: torch.Tensor, eps: float = 1e-5):
         self.layer, self.gamma, self.eps = layer, gamma, eps
@@ -156,10 +158,12 @@ class MoEBlock:
         n, s = rmsnorm(x, self.gamma, self.eps, residual=residual)
         if residual is None:
             s = x.contiguous()
+        most = getattr(self.layer, "few_max_tokens", None)
+        if most is None:  # an expert-parallel layer
+            return _on(x, self.layer.forward, n), s
         T = x.shape[0]
         if T == 0:
             return n, s
-        few = T <= self.layer.few_max_tokens
-        return _on(x, self.layer.forward_few if few else self.layer.forward, n), s
+        return _on(x, self.layer.forward_few if T <= most else self.layer.forward, n), s
 
     __call__ = forward

@@ -35,6 +35,19 @@ class _Layer:
         return 2 * n
 
 
+class _Sharded:
+    """As ExpertParallelMoE: every rank's call takes part, tokens or not."""
+
+    def __init__(self):
+        self.calls = []
+
+    def forward(self, n):
+        self.calls.append(n.shape[0])
+        return 2 * n
+
+    __call__ = forward
+
+
 def _rows(T, seed=0):
     return torch.randn((T, 64), generator=torch.Generator().manual_seed(seed)).to(BF16)
 
@@ -59,3 +72,12 @@ def test_few_and_many_tokens(plain):
         y, s = block.MoEBlock(layer, gamma)(_rows(T), _rows(T, 1))
         assert y.shape == s.shape == (T, 64)
     assert layer.calls == [("few", 1), ("few", 4), ("forward", 5)]
+
+
+def test_expert_parallel_layer(plain):
+    layer, gamma = _Sharded(), torch.ones(64, dtype=BF16)
+    for T in (0, 1, 5):
+        x, r = _rows(T), _rows(T, 1)
+        y, s = block.MoEBlock(layer, gamma)(x, r)
+        assert torch.equal(y, 2 * block.rmsnorm(x, gamma, residual=r)[0])
+    assert layer.calls == [0, 1, 5]

@@ -56,3 +56,23 @@ def test_ep_one_rank_matches_single_gpu_layer(nccl_group, T, D, E, k, I, wfmt):
     assert torch.equal(y.view(torch.int16), y_ref.view(torch.int16))
     # a rank without tokens of its own returns an empty result and still serves its experts
     assert layer(inp.x[:0]).shape == (0, D)
+
+
+def test_block_with_the_expert_parallel_layer(nccl_group):
+    # the norm in front of a sharded layer, with and without tokens, and on a
+    # stream of the caller's
+    inp = synthetic.make_custom(40, 320, 8, 2, 192, seed=11, device="cuda", reject=oracle.gap_reject())
+    weights = (inp.Wr, inp.br, inp.W1, inp.b1, inp.W2, inp.b2, 2)
+    gamma = torch.linspace(0.5, 1.5, 320, device="cuda").to(torch.bfloat16)
+    residual = torch.randn((40, 320), device="cuda").to(torch.bfloat16)
+    run = moe.MoEBlock(moe.ExpertParallelMoE(*weights, group=nccl_group), gamma)
+    want = moe.MoEBlock(moe.MoELayer(*weights), gamma)(inp.x, residual)  # (40 tokens: the batched layer)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (None, side):
+        got = run(inp.x, residual, stream=stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    y, s = run(inp.x[:0], residual[:0])
+    assert y.shape == s.shape == (0, 320)
+    assert run.layer.ops.device_status() == 0

@@ -378,3 +378,92 @@ def test_infinite_hidden_unit_beside_large_finite_ones(T, wfmt):
     want = torch.full((T, D), float("inf"), dtype=BF16, device="cuda")
     want[:, 1::2] *= -1
     assert torch.equal(y, want)
+
+
+def _every_pass(cases, passes, run):
+    """run(workspaces, outputs) fills `passes` outputs of each case, every one of
+    which is compared with that of a single call."""
+    want = [_few(c) for c in cases]
+    outs = [[torch.zeros_like(y) for _ in range(passes)] for y, _ in want]
+    torch.cuda.synchronize()
+    run([ws for _, ws in want], outs)
+    torch.cuda.synchronize()
+    for (y, ws), got in zip(want, outs):
+        assert moe.moe_read_device_status(ws) == 0
+        assert all(torch.equal(out, y) for out in got)
+
+
+def test_two_streams_every_pass():
+    cases = [_make(4, 512, 16, 4, 512, "bf16"), _make(11, 512, 16, 4, 512, "mxfp4")]
+    streams = [torch.cuda.Stream() for _ in cases]
+
+    def run(spaces, outs):
+        for i in range(200):
+            for c, ws, out, stream in zip(cases, spaces, outs, streams):
+                _few(c, ws=ws, y=out[i], stream=stream)
+
+    _every_pass(cases, 200, run)
+
+
+def test_two_graphs_on_one_workspace_every_pass():
+    cases = [_make(4, 512, 16, 4, 512, "bf16"), _make(11, 512, 16, 4, 512, "mxfp4")]
+    shared = torch.zeros(max(moe.workspace_bytes(dims_of(c)) for c in cases), dtype=torch.uint8, device="cuda")
+
+    def run(_, outs):
+        graphs, into = [], [torch.zeros_like(out[0]) for out in outs]
+        for c, y in zip(cases, into):
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1]):
+                _few(c, ws=shared, y=y)
+        for i in range(100):
+            for graph, y, out in zip(graphs, into, outs):
+                graph.replay()
+                out[i].copy_(y)
+
+    _every_pass(cases, 100, run)
+    assert moe.moe_read_device_status(shared) == 0
+
+
+def test_two_graphs_at_once_every_pass():
+    cases = [_make(2, 512, 16, 4, 512, "mxfp4"), _make(9, 448, 8, 2, 704, "bf16")]
+    streams = [torch.cuda.Stream() for _ in cases]
+
+    def run(spaces, outs):
+        graphs = []
+        for c, ws, out in zip(cases, spaces, outs):
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1]):
+                for y in out:
+                    _few(c, ws=ws, y=y)
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for graph, stream in zip(graphs, streams):
+                with torch.cuda.stream(stream):
+                    graph.replay()
+
+    _every_pass(cases, 20, run)
+
+
+def test_two_host_threads_every_pass():
+    import threading
+    cases = [_make(1, 512, 16, 4, 512, "mxfp4"), _make(7, 1024, 16, 4, 2048, "mxfp4")]
+    failed = []
+
+    def run(spaces, outs):
+        def calls(inp, ws, out):
+            try:
+                stream = torch.cuda.Stream()
+                for y in out:
+                    _few(inp, ws=ws, y=y, stream=stream)
+                stream.synchronize()
+            except Exception as err:
+                failed.append(repr(err))
+
+        threads = [threading.Thread(target=calls, args=a) for a in zip(cases, spaces, outs)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+
+    _every_pass(cases, 100, run)
+    assert failed == []

@@ -547,21 +547,26 @@ moe_status_t launch_fp8_matmul(const moe_fp8_t& d, const uint8_t* a, const float
   p.bias = bias;
   p.out = out;
   p.status = status;
-  // The tile whose rounds over the SMs cost least: a block of K takes 0.68 us at
-  // 256 columns (0.82 where tiles have few rows and the weights' stream sets the
-  // time), 0.64 at 192, 0.36 at 64 (measured at 8192 x 5760 and on 9 rows an
-  // expert); rounds are estimated from the row tiles, half a round for the tail.
-  // So long batches take 256 columns (8192 x 5760 x 2880: 155 us against 191 at
-  // 192), decode batches of many experts 192 (256 rows on 32 experts of 2880 x
-  // 2880: 51 us against 66 at 128 and 78 at 64), single decode projections 64
-  // (17 x 5760 x 2880: 14.8 us against 18.4 at 192).
+  // The tile whose rounds over the SMs cost least: a block of K takes 0.62 us at
+  // 256 columns (0.66 where tiles have few rows and the weights' stream sets the
+  // time), 0.54 at 192, 0.29 at 64. Rounds are whole ones for a dense product; for
+  // several experts, whose rows the host does not know, they are estimated, with
+  // half a round for the tail. Measured in us at 256 / 192 / 64 columns, a launch
+  // among others on operands that the L2 has not, on both sides of the borders.
+  // 5760 columns, K = 2880: 128 rows 16.8 / 16.0 / 11.5, 200 rows 17.1 / 16.0 / 18.5,
+  // 1024 rows 30.3 / 27.2 / 37.6, 1536 rows 30.4 / 38.9 / 56.6, 8192 rows 147 / 162 /
+  // 264. 32 experts (28 with rows) of 2880 x 2880: 256 rows 53.5 / 48.3 / 69.8, 4096
+  // rows 69.2 / 74.7 / 107; 8 of 4096 x 4096: 8 rows 22.8 / 22.2 / 26.6, 256 rows 27.8
+  // / 39.4 / 41.8. Over 120 sizes, up to 16384 rows and 128 experts, the chosen tile
+  // takes 0.6% more than the best on average, 16% at worst.
   const bool few = d.R < 64LL * d.E;
-  const int64_t mtiles = few ? std::min(d.E, d.R) : d.R / 128 + d.E;
+  const int64_t mtiles = d.E == 1 ? (d.R + 127) / 128 : few ? std::min(d.E, d.R) : d.R / 128 + d.E;
   auto cost = [&](int bn, double us) {
-    const double rounds = static_cast<double>(mtiles * ((d.N + bn - 1) / bn)) / num_sms() + 0.5;
-    return us * (rounds < 1.0 ? 1.0 : rounds);
+    const int64_t tiles = mtiles * ((d.N + bn - 1) / bn);
+    if (d.E == 1) return us * static_cast<double>((tiles + num_sms() - 1) / num_sms());
+    return us * std::max(1.0, static_cast<double>(tiles) / num_sms() + 0.5);
   };
-  const double c256 = cost(256, few ? 0.82 : 0.68), c192 = cost(192, 0.64), c64 = cost(64, 0.36);
+  const double c256 = cost(256, few ? 0.66 : 0.62), c192 = cost(192, 0.54), c64 = cost(64, 0.29);
   if (c64 <= c192 && c64 <= c256) return launch<Shape<64, 4>>(p, a, w, s);
   if (c192 <= c256) return launch<Shape<192, 12>>(p, a, w, s);
   return launch<Shape<256, 8>>(p, a, w, s);

@@ -164,3 +164,19 @@ def test_norm_feeds_the_product():
     y = (s.double() / torch.sqrt(s.double().pow(2).mean(1, keepdim=True) + 1e-5))
     c = scale.double().repeat_interleave(128, 1)[:, :D]
     assert bool(((q.to(F32).double() * c - y).abs() <= (2.0 ** -4 + 2.0 ** -16) * y.abs().maximum(2.0 ** -6 * c)).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("counts,N,K", [
+    ([200], 5760, 272),                     # dense, tiles of 192 columns: one round, where 64 would take two
+    ([700], 4112, 144),                     # 192, ragged rows and columns
+    ([0, 11, 7] * 10 + [33, 129], 2880, 400),  # grouped, 192
+    ([8, 0, 40, 31, 33, 1, 9, 7], 4096, 272),  # few rows, 256
+    ([130, 0, 257, 90], 4096, 272),         # more, 256
+    ([3, 1], 272, 1040),                    # 64
+])
+def test_tiles_on_both_sides_of_the_rule(counts, N, K, dtype):
+    offsets = [0]
+    for c in counts:
+        offsets.append(offsets[-1] + c)
+    _run(offsets[-1], len(counts), N, K, offsets, dtype, seed=5)

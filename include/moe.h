@@ -209,9 +209,11 @@ MOE_API moe_status_t moe_forward(moe_dims_t d, const uint16_t* x, const uint16_t
  * One cooperative kernel streams the weights of the experts the tokens route
  * to once, as stored (bf16, or MXFP4 codes and scales: data and scales are
  * required, a prepared form is not read). Logits and expert outputs are fp32,
- * h is rounded to bf16; MXFP4 codes are multiplied exactly with activations
- * that keep bf16's precision, so the output is that of the dequantised
- * weights (a scale byte of 0, 2^-127, counts as zero; 255 is an infinity).
+ * h is rounded to bf16. MXFP4 codes are multiplied exactly with activations
+ * held as f16 times a power of two per row: exact down to 2^-25 of the row's
+ * largest magnitude, off by less than 2^-33 of it below that. So the output is
+ * that of the dequantised weights (a scale byte of 0, 2^-127, counts as zero;
+ * 255 is an infinity).
  * Equal logits go to the lower expert index, a NaN logit below every
  * number; an infinity or NaN in a token's row reaches only that token's
  * output. x and y must not overlap. Deterministic for given sizes; its sums

@@ -54,18 +54,21 @@
 // Measured, D = I = 2880, top-4 (the weights' bytes at the measured copy rate in
 // brackets; a kernel that only reads needs 36 us for one token's 199 MB of bf16
 // weights and about 15 for its 53 MB of MXFP4): 32 experts, bf16, 1 token 48 us
-// (30), 16 tokens 242 (220); MXFP4, 1 token 27 us (8); 128 experts, MXFP4, 7
-// tokens 78 us (52). What is left: about 6 us in front of one token's weights (9
-// for 7 tokens and 128 experts: router, barrier, lists), 2 us at each later
-// barrier and 2 to 3 of SMs that end unequally; MXFP4 turns take 2.3 us where the
-// memory needs 2.2. The loop over the two weights is unrolled: 81 -> 78 us,
-// though mlp2's first turn then fetches its code (1.5 us). Measured and not kept: 24 warps for MXFP4 (72 registers:
-// no faster), a granule a stage (94 -> 108 us: twice the hand-overs), codes without
-// bank conflicts by exchanging units in registers (94 -> 102: the shared memory is
-// not what bounds), two granules per warp sharing the activations' loads (mlp1 41
-// -> 49 us), row-by-row copies of codes that lie well (60 ns each: 49 -> 60), a
-// router worked out by every block in place of the first barrier (4.1 -> 10.9 us:
-// every SM reads the same weights from cold).
+// (30), 16 tokens 239 to 257 (212 to 235); MXFP4, 1 token 27 us (8); 128 experts,
+// MXFP4, 7 tokens 75 to 83 us (50 to 56). What is left: about 5 us in front of one
+// token's weights (9 for 7 tokens and 128 experts: router, barrier, lists), 2 us at
+// each later barrier and 2 to 4 of SMs that end unequally; MXFP4 turns take 2.2 us,
+// what the memory needs, but mlp2's first, which also brings the rows of h, ends 6.5
+// us after the barrier. The loop over the two weights is unrolled, 81 -> 78 us,
+// although every SM then fetches another code for mlp2. Codes copied row by row are
+// further from the memory's rate: 8 tokens, D = I = 4096, 7 of 8 experts 65 us (28),
+// D = 7168, I = 2048, 21 of 32 experts 146 us (76). Measured and not kept: 24 warps
+// for MXFP4 (72 registers: no faster), a granule a stage (94 -> 108 us: twice the
+// hand-overs), codes without bank conflicts by exchanging units in registers (94 ->
+// 102: the shared memory is not what bounds), two granules per warp sharing the
+// activations' loads (mlp1 41 -> 49 us), row-by-row copies of codes that lie well
+// (60 ns each: 49 -> 60), a router worked out by every block in place of the first
+// barrier (4.1 -> 10.9 us: every SM reads the same weights from cold).
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -596,7 +599,6 @@ __device__ __forceinline__ void load_rows(const FewParams& p, FewShared& sh, con
   const int per = K / 8;  // 16-byte chunks per row
   constexpr int kAtOnce = 4;  // rows in flight
   for (int n0 = 0; n0 < rows; n0 += kAtOnce) {
-    if (kHere && kFmt == MOE_W_BF16) break;
     for (int base = threadIdx.x & ~31; base < per; base += kThreads) {  // (uniform in a warp)
       const int c = base + (threadIdx.x & 31);
       uint4 v[kAtOnce];
@@ -769,7 +771,7 @@ __global__ void __launch_bounds__(kThreads + (kFmt == MOE_W_MXFP4 ? 32 * kLoader
     }
   }
   grid_arrive(p.header, kBar1);
-  load_rows<kFmt, true>(p, sh, p.x, p.T, p.D, act);  // while the others arrive
+  if constexpr (kFmt == MOE_W_MXFP4) load_rows<kFmt, true>(p, sh, p.x, p.T, p.D, act);  // while the others arrive
   grid_wait(p.header, kBar1);
 
   // ---- top-k of every token (warp t), then the active experts

@@ -13,9 +13,10 @@
 // handed over block by block through two TMEM buffers, 140 (1.9 PFLOP/s in a
 // burst; 168 us under the power cap). A buffer's round -- products, commit, wait,
 // read, release, wait -- bounds it: the hand-overs of a block alone take some 1000
-// cycles, the read 400, the products 512. Few rows are bound by the weights: 256
-// rows on 28 of 32 experts of 2880 x 2880 take 47 us (4.9 TB/s; 56 with cold
-// caches).
+// cycles, the read 400, the products 512. Few rows: 256 on 28 of 32 experts of
+// 2880 x 2880 take 48 us (4.8 TB/s; 56 with cold caches), 17 x 5760 x 2880 11 us. All
+// of a tile's 128 rows are multiplied, summed and kept room for in the ring, however
+// few there are, and 90 SMs have a tile of 64 of 5760 columns.
 //
 // Measured and not kept: halves of a tile handed over separately (157 us against
 // 145), CTA pairs (291 us: both hand-overs of every block then cross CTAs),

@@ -40,10 +40,14 @@ class MoELayer:
     bf16. Weights: Wr (E,D), br (E), W1 (E,2I,D),
     b1 (E,2I), W2 (E,D,I), b2 (E,D) bf16 -- or W1/W2 as MXFP4 codes with
     ``W1_scales``/``W2_scales``. ``act`` is MOE_ACT_SWIGLU or MOE_ACT_GPTOSS
-    (with the caller's ``act_alpha`` and ``act_limit``)."""
+    (with the caller's ``act_alpha`` and ``act_limit``). All of them dense and on
+    one device. One layer serves one stream at a time."""
 
     def __init__(self, Wr, br, W1, b1, W2, b2, k: int, W1_scales=None, W2_scales=None, act=MOE_ACT_SWIGLU,
                  act_alpha: float = 1.0, act_limit: float = float("inf")):
+        for t in (Wr, br, W1, b1, W2, b2, W1_scales, W2_scales):
+            if t is not None and (t.device != Wr.device or not t.is_contiguous()):
+                raise ValueError("weights must be contiguous and on one device")
         self.Wr, self.br, self.W1, self.b1, self.W2, self.b2 = Wr, br, W1, b1, W2, b2
         self.W1_scales, self.W2_scales = W1_scales, W2_scales
         self.k = k

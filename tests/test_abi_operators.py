@@ -143,3 +143,19 @@ def test_fp8_tensor_checks():
                 dict(out_dtype=torch.float16), dict(a_scale=torch.zeros((2, 4)).t())):
         with pytest.raises(ValueError):
             moe.fp8_matmul(**{**ok, **bad})
+
+
+def test_layer_weights_are_dense_and_on_one_device():
+    # the kernels read them by their addresses alone
+    E, D, I = 4, 64, 64
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    ok = dict(Wr=z(E, D), br=z(E), W1=z(E, 2 * I, D), b1=z(E, 2 * I), W2=z(E, D, I), b2=z(E, D))
+    moe.MoELayer(**ok, k=2)
+    for name, t in ok.items():
+        wide = z(*t.shape[:-1], 2 * t.shape[-1])[..., ::2]
+        for bad in (t.to("meta"), wide):
+            with pytest.raises(ValueError):
+                moe.MoELayer(**{**ok, name: bad}, k=2)
+    with pytest.raises(ValueError):
+        moe.MoELayer(**ok, k=2, W1_scales=torch.zeros((E, 2 * I, 2), dtype=torch.uint8, device="meta"),
+                     W2_scales=torch.zeros((E, D, 2), dtype=torch.uint8))

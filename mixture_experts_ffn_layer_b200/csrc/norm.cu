@@ -13,7 +13,7 @@
 //
 // Memory bound: x, the residual and the outputs each cross once. 8192 x 2880
 // with a bf16 residual takes 32.5 us (5.8 TB/s, 88% of the measured copy rate),
-// 16384 x 2880 with E4M3 output 55.5 us (6.0 TB/s, 91%). A persistent grid whose
+// 16384 x 2880 with E4M3 output 55.7 us (6.0 TB/s, 91%). A persistent grid whose
 // blocks load the next row while they finish one was no faster (33.1 and 55.4 us
 // at 1536 threads an SM, 41.3 and 72.0 at 1024): with 34 registers a thread ten
 // blocks share an SM and overlap each other.

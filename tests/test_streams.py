@@ -161,3 +161,30 @@ def test_norm_and_product_on_another_stream():
         torch.cuda.synchronize()
         assert all(float(v) == T * D for v in sums)
         assert torch.equal(out, want) and torch.equal(y, moe.rmsnorm(x, gamma)[0])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 40])
+def test_block_on_a_forked_stream_of_a_capture(T):
+    g = torch.Generator(device="cuda").manual_seed(T)
+    rand = lambda *s: torch.randn(s, generator=g, device="cuda").to(BF16)
+    E, D, I = 8, 320, 192
+    layer = moe.MoELayer(rand(E, D), rand(E), rand(E, 2 * I, D), rand(E, 2 * I), rand(E, D, I), rand(E, D), 2)
+    run = moe.MoEBlock(layer, 1 + rand(D))
+    x, residual = rand(T, D), rand(T, D)
+    want_y, want_s = run(x, residual)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        y, s = run(x, residual, stream=side)
+        here.wait_stream(side)
+        y2, s2 = run(y, s)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want_y) and torch.equal(s, want_s)
+        again = run(want_y, want_s)
+        assert torch.equal(y2, again[0]) and torch.equal(s2, again[1])
+    assert layer.device_status() == 0
